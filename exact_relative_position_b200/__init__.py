@@ -5,12 +5,18 @@
 Shaw (truncated), Transformer-XL (identity), DeBERTa (log buckets) and T5
 (buckets) relative attention, forward and backward, computed by the CUDA
 library behind the C ABI in include/relpos_attn.h.  PyTorch supplies device
-memory and streams only.
+memory and streams only.  For generation: a paged K/V cache in 16 or 8 bits,
+attention of drafted tokens over it with the same relation terms, and rotary
+embedding (`serving`).
 """
 from ._binding import (  # noqa: F401
     RelPosError, RelPosMap, check_noalloc, check_workspace, debug_phi, debug_phi_device, debug_projection,
     debug_tile_plan, debug_tile_plan_device, expanded_bounds, kernel_launches, lib, profile_start, profile_stop,
     relpos_attn_bwd, relpos_attn_fwd, set_wait_limit_ns, sum_partials, table_rows, workspace_size,
+)
+from .serving import (  # noqa: F401
+    KVCache, RotaryMap, kv_cache, kv_cache_read, kv_cache_write, relpos_rotary, relpos_tree_attention,
+    rotary_embedding, tree_masks, tree_workspace_size,
 )
 
 import torch

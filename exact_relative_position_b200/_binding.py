@@ -64,12 +64,55 @@ class relpos_phase_stat(ctypes.Structure):
                 ("total_ms", ctypes.c_float)]
 
 
+class relpos_rotary_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int32), ("pad", ctypes.c_int32),
+                *[(f"{t}_stride_{i}", ctypes.c_int64) for t in "xy" for i in "bhn"]]
+
+
+class relpos_rotary_args(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("magnitude", ctypes.c_float), ("position_bytes", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("position_stride_b", ctypes.c_int64), ("steps", ctypes.c_void_p),
+                ("t", relpos_rotary_tensor * 2)]
+
+
+class relpos_kv_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("format", ctypes.c_int32), ("pad", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class relpos_cache_write_args(ctypes.Structure):
+    _fields_ = [("cache", relpos_kv_cache), ("B", ctypes.c_int32), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("pad", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                *[(f"{t}_stride_{i}", ctypes.c_int64) for t in "kv" for i in "bhn"], ("slots", ctypes.c_void_p)]
+
+
+class relpos_cache_read_args(ctypes.Structure):
+    _fields_ = [("cache", relpos_kv_cache), ("B", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class relpos_tree_args(ctypes.Structure):
+    _fields_ = [("cache", relpos_kv_cache), ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("pad", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("tau", ctypes.c_float), ("max_seqlen", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("table_per_head", ctypes.c_int32), ("map", relpos_map_desc), ("mask_per_seq", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                *[(f"{t}_stride_{i}", ctypes.c_int64) for t in "qkv" for i in "bhn"], ("aq", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
 EXPORTS = ["relpos_table_rows", "relpos_expanded_bounds", "relpos_workspace_size", "relpos_attn_fwd",
            "relpos_attn_bwd", "relpos_status_string", "relpos_last_cuda_error", "relpos_debug_phi",
            "relpos_debug_phi_device", "relpos_debug_tile_plan", "relpos_debug_tile_plan_device",
            "relpos_profile_start", "relpos_profile_stop", "relpos_kernel_launches", "relpos_attn_fwd_noalloc",
            "relpos_check_workspace", "relpos_sum_partials", "relpos_check_noalloc", "relpos_debug_projection",
-           "relpos_set_wait_limit_ns"]
+           "relpos_set_wait_limit_ns", "relpos_rotary", "relpos_cache_write", "relpos_cache_read",
+           "relpos_tree_workspace_size", "relpos_tree_attn"]
 
 
 def load_library(path: str = LIBPATH) -> ctypes.CDLL:
@@ -102,6 +145,11 @@ def load_library(path: str = LIBPATH) -> ctypes.CDLL:
     sig["relpos_debug_projection"] = [P(relpos_fwd_args), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                       P(relpos_projection_layout)]
     sig["relpos_set_wait_limit_ns"] = [ctypes.c_uint64]
+    sig["relpos_rotary"] = [P(relpos_rotary_args), ctypes.c_void_p]
+    sig["relpos_cache_write"] = [P(relpos_cache_write_args), ctypes.c_void_p]
+    sig["relpos_cache_read"] = [P(relpos_cache_read_args), ctypes.c_void_p]
+    sig["relpos_tree_workspace_size"] = [P(relpos_tree_args), P(ctypes.c_size_t)]
+    sig["relpos_tree_attn"] = [P(relpos_tree_args), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args

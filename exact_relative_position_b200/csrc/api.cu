@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "kernels.cuh"
+#include "serve.cuh"
 #include "sm100.cuh"
 
 #define RELPOS_EXPORT extern "C" __attribute__((visibility("default")))
@@ -38,9 +39,11 @@ int relpos::cuda_status(cudaError_t e) { return cuda_fail(e); }
 namespace {
 
 // ---- optional per-phase event timing (relpos_profile_start / _stop)
-enum Phase { PH_TABLES, PH_PROJ, PH_FWD, PH_PREP, PH_DQ, PH_DKDV, PH_FOLD, PH_RELGRAD, PH_BWD_ATTN, PH_COUNT };
+enum Phase { PH_TABLES, PH_PROJ, PH_FWD, PH_PREP, PH_DQ, PH_DKDV, PH_FOLD, PH_RELGRAD, PH_BWD_ATTN,
+             PH_ROTARY, PH_CACHE_WRITE, PH_CACHE_READ, PH_TREE_REL, PH_TREE, PH_COUNT };
 const char* const kPhaseNames[PH_COUNT] = {"tables",  "projection", "fwd_attention", "bwd_prep",     "bwd_dq",
-                                           "bwd_dkdv", "fold_ranges", "relation_grads", "bwd_attention"};
+                                           "bwd_dkdv", "fold_ranges", "relation_grads", "bwd_attention",
+                                           "rotary", "cache_write", "cache_read", "tree_relation", "tree_attention"};
 // Duration a -> b, or a -> the later of b and c when c is set (two streams).
 struct PhaseEvent {
   int phase, kernels;
@@ -769,5 +772,243 @@ RELPOS_EXPORT int relpos_debug_tile_plan_device(const relpos_map_desc* map, int3
                                          (mask & RELPOS_MASK_KEY_PADDING) ? key_len_dev : nullptr, lo, hi,
                                          classes_dev, segs_dev, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e == cudaSuccess ? RELPOS_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------- rotary, K/V cache, tree attention
+namespace {
+
+Strides strides(int64_t b, int64_t h, int64_t n) { return Strides{(long long)b, (long long)h, (long long)n}; }
+bool rows16(const Strides& s) { return s.b % 8 == 0 && s.h % 8 == 0 && s.n % 8 == 0; }
+
+int check_cache(const relpos_kv_cache& c, CacheParams* p) {
+  if (c.format < RELPOS_CACHE_F16 || c.format > RELPOS_CACHE_INT8) return RELPOS_ERR_UNSUPPORTED;
+  if (c.num_pages < 1 || c.kv_heads < 1 || c.page_size < 1 || c.page_size > 65536) return RELPOS_ERR_INVALID_ARG;
+  if (c.page_size & (c.page_size - 1)) return RELPOS_ERR_INVALID_ARG;
+  if (c.d < 16 || c.d > 256 || c.d % 16) return RELPOS_ERR_UNSUPPORTED;
+  // rows of the cache are numbered in 32 bits, all ones meaning none
+  if ((unsigned long long)c.num_pages * c.kv_heads > 0xfffffffeull / c.page_size) return RELPOS_ERR_INVALID_ARG;
+  const bool coded = c.format == RELPOS_CACHE_E4M3 || c.format == RELPOS_CACHE_INT8;
+  if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v)) return RELPOS_ERR_INVALID_ARG;
+  if (coded && (!c.k_scale || !c.v_scale)) return RELPOS_ERR_INVALID_ARG;
+  if (coded && ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 3))
+    return RELPOS_ERR_INVALID_ARG;
+  p->k = c.k; p->v = c.v; p->ks = c.k_scale; p->vs = c.v_scale;
+  p->num_pages = c.num_pages;
+  p->page_shift = __builtin_ctz((unsigned)c.page_size);
+  p->Hkv = c.kv_heads; p->d = c.d; p->format = c.format;
+  return RELPOS_OK;
+}
+
+bool is16(int dtype) { return dtype == RELPOS_F16 || dtype == RELPOS_BF16; }
+bool wide_cache(int format) { return format == RELPOS_CACHE_F16 || format == RELPOS_CACHE_BF16; }
+bool same_type(int format, int dtype) { return (format == RELPOS_CACHE_BF16) == (dtype == RELPOS_BF16); }
+
+// Saturation bounds of a map.  Offsets beyond max_distance share a row, so a
+// bucketed map is scanned over that many at most; the last map's bounds are kept
+// per thread, since a decoder asks for the same ones at every step.
+void map_bounds(const relpos_map_desc& m, int N, int* lo, int* hi) {
+  if (m.kind == RELPOS_MAP_TRUNCATED || m.kind == RELPOS_MAP_IDENTITY) return bounds_of(m, N, lo, hi);
+  const int n = (int)std::min<long long>(N, (long long)m.max_distance + 2);
+  struct Memo { relpos_map_desc m; int n, lo, hi; };
+  static thread_local Memo memo = {{-1, 0, 0, 0, 0}, 0, 0, 0};
+  if (memo.n != n || memcmp(&memo.m, &m, sizeof(m)) != 0) {
+    bounds_of(m, n, &memo.lo, &memo.hi);
+    memo.m = m;
+    memo.n = n;
+  }
+  *lo = memo.lo;
+  *hi = memo.hi;
+}
+
+struct TreeLayout {
+  size_t part, z, end;
+  int grid;
+};
+
+int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
+  if (!a) return RELPOS_ERR_INVALID_ARG;
+  memset(p, 0, sizeof(*p));
+  if (a->cache.d != 64 && a->cache.d != 128) return RELPOS_ERR_UNSUPPORTED;
+  int st = check_cache(a->cache, &p->c);
+  if (st) return st;
+  if (!is16(a->dtype)) return RELPOS_ERR_UNSUPPORTED;
+  if (a->out_dtype != a->dtype && a->out_dtype != RELPOS_F32) return RELPOS_ERR_UNSUPPORTED;
+  if (wide_cache(a->cache.format) && !same_type(a->cache.format, a->dtype)) return RELPOS_ERR_UNSUPPORTED;
+  if (a->B < 1 || a->B > 4096 || a->T < 1 || a->T > 64 || a->H < 1 || a->H > 65535) return RELPOS_ERR_INVALID_ARG;
+  if (a->H % a->cache.kv_heads || a->pages_per_seq < 1) return RELPOS_ERR_INVALID_ARG;
+  if (!(a->tau > 0.f) || a->tau > 3.0e38f) return RELPOS_ERR_INVALID_ARG;
+  const long long cap = (long long)a->pages_per_seq * a->cache.page_size;
+  if (cap > (1LL << 30)) return RELPOS_ERR_INVALID_ARG;
+  // tiles are counted in 32 bits
+  if ((cap / 32 + 4) * a->B > 0x7fffffffLL) return RELPOS_ERR_INVALID_ARG;
+  p->B = a->B; p->T = a->T; p->H = a->H; p->G = a->H / a->cache.kv_heads;
+  p->bf16 = a->dtype == RELPOS_BF16;
+  p->o_f32 = a->out_dtype == RELPOS_F32;
+  p->page_table = a->page_table; p->P = a->pages_per_seq; p->lengths = a->lengths;
+  p->mask = reinterpret_cast<const long long*>(a->tree_mask);
+  p->mask_bs = a->mask_per_seq ? a->T : 0;
+  p->q = a->q; p->k = a->k; p->v = a->v;
+  p->qs = strides(a->q_stride_b, a->q_stride_h, a->q_stride_n);
+  p->ks = strides(a->k_stride_b, a->k_stride_h, a->k_stride_n);
+  p->vs = strides(a->v_stride_b, a->v_stride_h, a->v_stride_n);
+  p->o = a->o; p->lse = a->lse;
+  p->c2 = a->tau * kLog2e;
+  const int rows = p->G * a->T;
+  p->rows_per_block = tree_rows_per_block(rows, a->cache.d);
+  p->row_blocks = (rows + p->rows_per_block - 1) / p->rows_per_block;
+  if ((long long)a->B * a->cache.kv_heads * p->row_blocks > 0x7fffffffLL) return RELPOS_ERR_INVALID_ARG;
+  p->grid = tree_grid(*p);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off = up256(off + bytes); return o; };
+  L->part = take(sizeof(float) * 2 * (size_t)p->grid * (size_t)p->rows_per_block * (a->cache.d + 2));
+  L->z = 0;
+  if (a->aq || a->b) {
+    st = check_map(&a->map);
+    if (st) return st;
+    if (a->max_seqlen < 1 || a->max_seqlen > kMaxN) return RELPOS_ERR_INVALID_ARG;
+    p->map = a->map;
+    p->N = a->max_seqlen;
+    p->R = rows_of(a->map, a->max_seqlen);
+    int lo, hi;
+    map_bounds(a->map, a->max_seqlen, &lo, &hi);
+    // the reachable part of the expanded range: cached keys lie up to cap + T behind
+    // a node, nodes up to T ahead
+    const int back = -(int)(cap + a->T), ahead = a->T;
+    if (lo > ahead) hi = lo;
+    else if (hi < back) lo = hi;
+    else { lo = std::max(lo, back); hi = std::min(hi, ahead); }
+    p->e_lo = lo; p->e_hi = hi;
+    const long long zw = ((long long)hi - lo + 1 + 7) & ~7LL;
+    p->aq = a->aq; p->bias = a->b;
+    p->aq_hs = a->table_per_head ? (long long)p->R * a->cache.d : 0;
+    p->z_scale = wide_cache(a->cache.format) ? 1.f : p->c2;
+    p->z_h = a->aq ? zw * a->T : zw;
+    p->z_t = a->aq ? zw : 0;
+    p->z_b = a->aq ? zw * a->T * a->H : 0;
+    L->z = take(sizeof(float) * (size_t)(a->aq ? p->z_b * a->B : zw * a->H));
+  }
+  L->end = off;
+  return RELPOS_OK;
+}
+
+}  // namespace
+
+RELPOS_EXPORT int relpos_rotary(const relpos_rotary_args* a, relpos_stream_t stream) {
+  if (!a || a->n_tensors < 1 || a->n_tensors > 2 || !a->steps) return RELPOS_ERR_INVALID_ARG;
+  if (a->B < 0 || a->N < 0 || a->d < 1) return RELPOS_ERR_INVALID_ARG;
+  if (a->rotary_dim < 2 || a->rotary_dim % 2 || a->rotary_dim > a->d || a->rotary_dim > 2 * kMaxPairs)
+    return RELPOS_ERR_INVALID_ARG;
+  if (a->dtype != RELPOS_F16 && a->dtype != RELPOS_BF16 && a->dtype != RELPOS_F32) return RELPOS_ERR_UNSUPPORTED;
+  if (a->position_bytes != 4 && a->position_bytes != 8) return RELPOS_ERR_INVALID_ARG;
+  if (a->positions && reinterpret_cast<uintptr_t>(a->positions) % a->position_bytes) return RELPOS_ERR_INVALID_ARG;
+  if (!(a->magnitude >= -3.0e38f && a->magnitude <= 3.0e38f)) return RELPOS_ERR_INVALID_ARG;
+  const int es = a->dtype == RELPOS_F32 ? 4 : 2;
+  RotaryParams p;
+  memset(&p, 0, sizeof(p));
+  p.n_tensors = a->n_tensors;
+  for (int i = 0; i < a->n_tensors; ++i) {
+    const relpos_rotary_tensor& t = a->t[i];
+    if (t.H < 0 || t.H > 65535) return RELPOS_ERR_INVALID_ARG;
+    const bool empty = t.H == 0 || a->B == 0 || a->N == 0;
+    if (!empty && (!t.x || !t.y)) return RELPOS_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(t.x) % es || reinterpret_cast<uintptr_t>(t.y) % es) return RELPOS_ERR_INVALID_ARG;
+    p.t[i].x = t.x; p.t[i].y = t.y; p.t[i].H = t.H;
+    p.t[i].xs = strides(t.x_stride_b, t.x_stride_h, t.x_stride_n);
+    p.t[i].ys = strides(t.y_stride_b, t.y_stride_h, t.y_stride_n);
+  }
+  if (a->B == 0 || a->N == 0 || p.t[0].H + p.t[1].H == 0) return RELPOS_OK;
+  p.B = a->B; p.N = a->N; p.d = a->d;
+  p.rotary_dim = a->rotary_dim; p.interleaved = a->interleaved != 0;
+  p.pos = a->positions; p.pos_wide = a->position_bytes == 8; p.pos_bs = a->position_stride_b;
+  p.cos_scale = a->magnitude;
+  p.sin_scale = a->inverse ? -a->magnitude : a->magnitude;
+  memcpy(p.step, a->steps, sizeof(uint64_t) * (a->rotary_dim / 2));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = run_phase(PH_ROTARY, s, [&] { return launch_rotary(p, es, a->dtype == RELPOS_BF16, s); });
+  return e == cudaSuccess ? RELPOS_OK : cuda_fail(e);
+}
+
+RELPOS_EXPORT int relpos_cache_write(const relpos_cache_write_args* a, relpos_stream_t stream) {
+  if (!a) return RELPOS_ERR_INVALID_ARG;
+  CacheWriteParams p;
+  memset(&p, 0, sizeof(p));
+  const int st = check_cache(a->cache, &p.c);
+  if (st) return st;
+  if (!is16(a->dtype)) return RELPOS_ERR_UNSUPPORTED;
+  if (wide_cache(a->cache.format) && !same_type(a->cache.format, a->dtype)) return RELPOS_ERR_UNSUPPORTED;
+  if (a->B < 0 || a->N < 0) return RELPOS_ERR_INVALID_ARG;
+  if (a->B == 0 || a->N == 0) return RELPOS_OK;
+  if (!a->k || !a->v || !a->slots || !aligned16(a->k) || !aligned16(a->v)) return RELPOS_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(a->slots) & 7) return RELPOS_ERR_INVALID_ARG;
+  p.k = a->k; p.v = a->v;
+  p.kst = strides(a->k_stride_b, a->k_stride_h, a->k_stride_n);
+  p.vst = strides(a->v_stride_b, a->v_stride_h, a->v_stride_n);
+  if (!rows16(p.kst) || !rows16(p.vst)) return RELPOS_ERR_INVALID_ARG;
+  if ((long long)a->B * a->N > (1LL << 31) / a->cache.kv_heads) return RELPOS_ERR_INVALID_ARG;
+  p.B = a->B; p.N = a->N;
+  p.slots = reinterpret_cast<const long long*>(a->slots);
+  p.bf16 = a->dtype == RELPOS_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = run_phase(PH_CACHE_WRITE, s, [&] { return launch_cache_write(p, s); });
+  return e == cudaSuccess ? RELPOS_OK : cuda_fail(e);
+}
+
+RELPOS_EXPORT int relpos_cache_read(const relpos_cache_read_args* a, relpos_stream_t stream) {
+  if (!a) return RELPOS_ERR_INVALID_ARG;
+  CacheReadParams p;
+  memset(&p, 0, sizeof(p));
+  const int st = check_cache(a->cache, &p.c);
+  if (st) return st;
+  if (!is16(a->dtype)) return RELPOS_ERR_UNSUPPORTED;
+  if (a->B < 1 || a->pages_per_seq < 0 || a->total_tokens < 0 || a->total_tokens > (1 << 30))
+    return RELPOS_ERR_INVALID_ARG;
+  if (a->total_tokens == 0) return RELPOS_OK;
+  if (!a->page_table || !a->cu_seqlens || !a->k || !a->v || !aligned16(a->k) || !aligned16(a->v))
+    return RELPOS_ERR_INVALID_ARG;
+  p.page_table = a->page_table; p.P = a->pages_per_seq; p.B = a->B;
+  p.cu = a->cu_seqlens; p.total = a->total_tokens;
+  p.k = a->k; p.v = a->v; p.bf16 = a->dtype == RELPOS_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = run_phase(PH_CACHE_READ, s, [&] { return launch_cache_read(p, s); });
+  return e == cudaSuccess ? RELPOS_OK : cuda_fail(e);
+}
+
+RELPOS_EXPORT int relpos_tree_workspace_size(const relpos_tree_args* a, size_t* bytes) {
+  if (!bytes) return RELPOS_ERR_INVALID_ARG;
+  TreeParams p;
+  TreeLayout L;
+  const int st = make_tree(a, &p, &L);
+  if (st) return st;
+  *bytes = L.end;
+  return RELPOS_OK;
+}
+
+RELPOS_EXPORT int relpos_tree_attn(const relpos_tree_args* a, void* workspace, size_t ws_bytes, relpos_stream_t stream) {
+  TreeParams p;
+  TreeLayout L;
+  const int st = make_tree(a, &p, &L);
+  if (st) return st;
+  if (!a->q || !a->k || !a->v || !a->o || !a->lse || !a->page_table || !a->lengths) return RELPOS_ERR_INVALID_ARG;
+  const void* al[] = {a->q, a->k, a->v, a->aq, a->o};
+  for (const void* x : al)
+    if (x && !aligned16(x)) return RELPOS_ERR_INVALID_ARG;
+  if (!rows16(p.qs) || !rows16(p.ks) || !rows16(p.vs)) return RELPOS_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(a->tree_mask) & 7) return RELPOS_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < L.end || (reinterpret_cast<uintptr_t>(workspace) & 255)) return RELPOS_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (a->aq || a->b) {
+    p.z = reinterpret_cast<float*>(ws + L.z);
+    e = run_phase(PH_TREE_REL, s, [&] { return launch_tree_relation(p, s); });
+  }
+  if (e == cudaSuccess)
+    e = run_phase(PH_TREE, s, [&] {
+      cudaError_t r = launch_tree_attention(p, s);
+      if (r == cudaSuccess) r = launch_tree_combine(p, s);
+      return r;
+    });
   return e == cudaSuccess ? RELPOS_OK : cuda_fail(e);
 }

@@ -1,0 +1,215 @@
+// tree_attn.cu -- the kernels around the tree attention (tree_attn.cuh): the
+// relation terms of the drafted queries, and the join of split items.
+#include "tree_attn.cuh"
+
+namespace relpos {
+namespace tree {
+namespace {
+
+// z[b, h, t, e] = z_scale (q . aQ[phi(e_lo + e)] + b[phi(e_lo + e)]): one MMA
+// product of a head's B T query rows with the table rows of the reachable
+// offsets.  A warp keeps 16 table rows in registers and walks over the rows
+// of queries, so the table is read once; z is written in fp32.  Offsets that no
+// row of 16 can reach (they lie before position 0) are left out.
+template <int D, typename QT>
+__global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ TreeParams p) {
+  const int lane = threadIdx.x & 31, q4 = lane & 3, r8 = lane >> 2;
+  const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 16;
+  const int W = p.e_hi - p.e_lo + 1;
+  if (c0 >= W) return;
+  const int h = blockIdx.y;
+  uint4 bw[2][D / 32];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = min(c0 + 8 * j + r8, W - 1);
+    const int r = iclamp(phi_of(p.map, p.N, p.e_lo + c), 0, p.R - 1);
+    const uint16_t* src = static_cast<const uint16_t*>(p.aq) + h * p.aq_hs + (long long)r * D;
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) bw[j][u] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u + 8 * q4));
+  }
+  float bias[2][2] = {};
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = min(c0 + 8 * j + 2 * q4 + c, W - 1);
+        bias[j][c] = p.bias[(long long)h * p.R + iclamp(phi_of(p.map, p.N, p.e_lo + col), 0, p.R - 1)];
+      }
+  }
+  const int rows = p.B * p.T;
+  for (int r0 = blockIdx.z * 16; r0 < rows; r0 += gridDim.z * 16) {
+    int rr[2], bb[2], tt[2];
+    bool need = false;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      rr[e] = r0 + r8 + 8 * e;
+      const int r = min(rr[e], rows - 1);
+      bb[e] = r / p.T;
+      tt[e] = r - bb[e] * p.T;
+      need = need || p.e_lo + c0 + 15 >= -(seq_len(p, bb[e]) + p.T);
+    }
+    if (!__any_sync(0xffffffffu, need)) continue;
+    float acc[2][4] = {};
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      uint4 w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        w[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + bb[e] * p.qs.b + h * p.qs.h +
+                                                    tt[e] * p.qs.n + 32 * u + 8 * q4));
+      const uint32_t a0[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, a1[4] = {w[0].z, w[1].z, w[0].w, w[1].w};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        MmaOp<QT>::run(acc[j], a0, bw[j][u].x, bw[j][u].y);
+        MmaOp<QT>::run(acc[j], a1, bw[j][u].z, bw[j][u].w);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (rr[e] >= rows) continue;
+      float* dst = p.z + bb[e] * p.z_b + h * p.z_h + tt[e] * p.z_t + c0 + 2 * q4;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (c0 + 8 * j + 2 * q4 < W)   // rows are padded to whole column tiles
+          *reinterpret_cast<float2*>(dst + 8 * j) = make_float2((acc[j][2 * e] + bias[j][0]) * p.z_scale,
+                                                                (acc[j][2 * e + 1] + bias[j][1]) * p.z_scale);
+    }
+  }
+}
+
+// The bias alone: one row of offsets a head, shared by sequences and nodes.
+__global__ void __launch_bounds__(128) bias_kernel(const __grid_constant__ TreeParams p) {
+  const int e = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;
+  if (e > p.e_hi - p.e_lo) return;
+  const int r = iclamp(phi_of(p.map, p.N, p.e_lo + e), 0, p.R - 1);
+  p.z[h * p.z_h + e] = p.bias[(long long)h * p.R + r] * p.z_scale;
+}
+
+// Joins the partial results of an item that was cut: pieces c0 .. c1 of the
+// line hold it, the first in the piece's last slot (unless the item begins the
+// piece), the others in their first.  Summed in the order of the pieces.
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p, int tk, int wide) {
+  __shared__ long long sums[2][4];
+  const int items = p.c.Hkv * p.row_blocks;
+  const int b = blockIdx.x / items, item = blockIdx.x - b * items;
+  const int tid = threadIdx.x;
+  long long before = 0, all = 0;
+  for (int i = tid; i < p.B; i += 128) {
+    const int n = seq_tiles(p, i, tk, wide);
+    all += n;
+    if (i < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if ((tid & 31) == 0) {
+    sums[0][tid >> 5] = before;
+    sums[1][tid >> 5] = all;
+  }
+  __syncthreads();
+  before = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
+  all = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
+  const long long total = all * items, quantum = (total + p.grid - 1) / p.grid;
+  const int nt = seq_tiles(p, b, tk, wide);
+  const long long start = before * items + (long long)item * nt;
+  const int c0 = (int)(start / quantum), c1 = (int)((start + nt - 1) / quantum);
+  if (c0 == c1) return;                                // written whole
+  const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
+  const int D = p.c.d, ROWS = p.rows_per_block;
+  const int first = start > c0 * quantum ? 1 : 0;
+  const long long sf = slot_floats(ROWS, D);
+  const int n = min(ROWS, p.G * p.T - rb * ROWS);
+  for (int i = tid; i < n * (D / 4); i += 128) {
+    const int r = i / (D / 4), c = i - r * (D / 4);
+    float m = -INFINITY;
+    for (int k = c0; k <= c1; ++k) m = fmaxf(m, p.part[(2LL * k + (k == c0 ? first : 0)) * sf + ROWS * D + r]);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = c0; k <= c1; ++k) {
+      const float* s = p.part + (2LL * k + (k == c0 ? first : 0)) * sf;
+      const float f = ex2(s[ROWS * D + r] - safe(m));
+      const float4 x = *reinterpret_cast<const float4*>(s + (long long)r * D + 4 * c);
+      l += s[ROWS * D + ROWS + r] * f;
+      o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+    }
+    store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
+  }
+}
+
+template <class TL> constexpr int blocks_of(bool wide) {
+  const int b = wide ? stage_bytes<TL, RELPOS_CACHE_F16>() : stage_bytes<TL, RELPOS_CACHE_INT8>();
+  const int fit = (227 * 1024 - 17 * 1024) / (b + 2048);   // 17 KB: the longest list of sequences
+  return fit < 4 ? fit : 4;
+}
+
+}  // namespace
+}  // namespace tree
+
+using namespace tree;
+
+int tree_rows_per_block(int rows, int d) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+int tree_tile_keys(int rows, int d) {
+  if (d == 64) return rows <= 16 ? T64_16::TK : rows <= 32 ? T64_32::TK : T64_64::TK;
+  return rows <= 16 ? T128_16::TK : rows <= 32 ? T128_32::TK : T128_64::TK;
+}
+
+// One piece of the line of tiles to each block that can be resident; fewer
+// where there are fewer tiles.
+int tree_grid(const TreeParams& p) {
+  const bool wide = p.c.format == RELPOS_CACHE_F16 || p.c.format == RELPOS_CACHE_BF16;
+  int per_sm;
+  if (p.c.d == 64)
+    per_sm = p.rows_per_block == 16 ? blocks_of<T64_16>(wide) : p.rows_per_block == 32 ? blocks_of<T64_32>(wide)
+                                                                                       : blocks_of<T64_64>(wide);
+  else
+    per_sm = p.rows_per_block == 16 ? blocks_of<T128_16>(wide) : p.rows_per_block == 32 ? blocks_of<T128_32>(wide)
+                                                                                        : blocks_of<T128_64>(wide);
+  const int tk = tree_tile_keys(p.rows_per_block, p.c.d);
+  const long long most = (((long long)p.P << p.c.page_shift) + p.T + tk - 1) / tk + 1;
+  const long long tiles = most * p.B * p.c.Hkv * p.row_blocks;
+  return (int)(tiles < 148LL * per_sm ? tiles : 148LL * per_sm);
+}
+
+cudaError_t launch_tree_relation(const TreeParams& p, cudaStream_t s) {
+  const int W = p.e_hi - p.e_lo + 1;
+  if (!p.aq) {
+    bias_kernel<<<dim3((W + 127) / 128, p.H), 128, 0, s>>>(p);
+  } else {
+    const int row_tiles = (p.B * p.T + 15) / 16, cols = (W + 63) / 64;
+    // walk the query rows in one block where the columns alone fill the card
+    int gz = (int)(148LL * 8 / ((long long)cols * p.H)) + 1;
+    gz = gz < row_tiles ? gz : row_tiles;
+    const dim3 grid(cols, p.H, gz);
+    if (p.c.d == 64) {
+      if (p.bf16) relation_kernel<64, __nv_bfloat16><<<grid, 128, 0, s>>>(p);
+      else relation_kernel<64, __half><<<grid, 128, 0, s>>>(p);
+    } else {
+      if (p.bf16) relation_kernel<128, __nv_bfloat16><<<grid, 128, 0, s>>>(p);
+      else relation_kernel<128, __half><<<grid, 128, 0, s>>>(p);
+    }
+  }
+  note_launch(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s) {
+  switch (p.c.format) {
+    case RELPOS_CACHE_F16: return run_f16(p, s);
+    case RELPOS_CACHE_BF16: return run_bf16(p, s);
+    case RELPOS_CACHE_E4M3: return p.bf16 ? run_e4m3_bf16(p, s) : run_e4m3_f16(p, s);
+    default: return p.bf16 ? run_int8_bf16(p, s) : run_int8_f16(p, s);
+  }
+}
+
+cudaError_t launch_tree_combine(const TreeParams& p, cudaStream_t s) {
+  const bool wide = p.c.format == RELPOS_CACHE_F16 || p.c.format == RELPOS_CACHE_BF16;
+  combine_kernel<<<p.B * p.c.Hkv * p.row_blocks, 128, 0, s>>>(p, tree_tile_keys(p.rows_per_block, p.c.d), wide);
+  note_launch(1);
+  return cudaGetLastError();
+}
+
+}  // namespace relpos

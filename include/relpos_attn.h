@@ -262,12 +262,155 @@ int relpos_attn_fwd_noalloc(const relpos_fwd_args* a, relpos_stream_t stream);
  * counterpart in the paper (failure report of the no-allocation forward). */
 int relpos_check_noalloc(relpos_stream_t stream, int32_t* device_status);
 
+/* --- rotary embedding ------------------------------------------------------ */
+
+/* A [B, H, N, d] view of 16- or 32-bit elements whose last dimension is
+ * contiguous; strides in elements.  A packed [T, H, d] tensor is the view with
+ * B = 1, N = T, stride_h = d, stride_n = H d. */
+typedef struct {
+  const void* x;             /* device, read */
+  void* y;                   /* device, written: x itself (same strides), or no overlap with x */
+  int32_t H, pad;
+  int64_t x_stride_b, x_stride_h, x_stride_n;
+  int64_t y_stride_b, y_stride_h, y_stride_n;
+} relpos_rotary_tensor;
+
+typedef struct {
+  int32_t n_tensors;         /* 1 or 2: tensors turned in one launch (queries and keys) */
+  int32_t B, N, d;           /* shared by the tensors; d >= 1 */
+  int32_t rotary_dim;        /* even, 2 .. min(d, 256): columns that are turned; the others are copied */
+  int32_t interleaved;       /* 1: pairs (2i, 2i + 1); 0: pairs (i, i + rotary_dim / 2) */
+  int32_t dtype;             /* RELPOS_F16, RELPOS_BF16 or RELPOS_F32 */
+  int32_t inverse;           /* 1: turn backwards (the gradient of the turn forwards) */
+  float magnitude;           /* finite; multiplies the turned columns */
+  int32_t position_bytes;    /* 4 (int32) or 8 (int64) */
+  const void* positions;     /* device [N] or [B, N] rows; NULL: token n has position n */
+  int64_t position_stride_b; /* elements between the positions of consecutive b; 0: shared */
+  const uint64_t* steps;     /* host [rotary_dim / 2]: turns per position, as a fraction of 2^64 */
+  relpos_rotary_tensor t[2];
+} relpos_rotary_args;
+
+/* Rotary position embedding (the third family of relative position terms next
+ * to tables and biases: q.k then depends on the offset alone):
+ *   y_a = m (x_a cos t - x_b sin t), y_b = m (x_b cos t + x_a sin t),
+ *   t = 2 pi position step / 2^64,
+ * computed in fp32 and rounded once.  `steps` is read before the call returns.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype), CUDA. */
+int relpos_rotary(const relpos_rotary_args* a, relpos_stream_t stream);
+
+/* --- paged K/V cache ------------------------------------------------------- */
+
+typedef enum {
+  RELPOS_CACHE_F16 = 0,      /* rows as they are */
+  RELPOS_CACHE_BF16 = 1,
+  RELPOS_CACHE_E4M3 = 2,     /* 8-bit float codes; scale = smallest power of two 2^s >= amax / 448, s >= -126 */
+  RELPOS_CACHE_INT8 = 3      /* 8-bit integer codes; scale = max(fl32(amax / 127), 2^-126) */
+} relpos_cache_format;
+
+/* A pool of pages.  Token `offset` of page p, key head h is row
+ * (p kv_heads + h) page_size + offset of k and v ([num_pages, kv_heads, page_size, d],
+ * contiguous) and entry of the scales ([num_pages, kv_heads, page_size]).  8-bit
+ * rows stand for code x scale; the codes are the nearest to x / scale, ties to
+ * even; a row of zeros has scale 1, a row with a non-finite value has scale
+ * NaN and codes 0. */
+typedef struct {
+  int32_t num_pages;         /* >= 1; num_pages kv_heads page_size < 2^32 - 1 */
+  int32_t page_size;         /* a power of two, 1 .. 65536 */
+  int32_t kv_heads, d;       /* d a multiple of 16, 16 .. 256 */
+  int32_t format;            /* relpos_cache_format */
+  int32_t pad;
+  void *k, *v;               /* device, 16-byte aligned */
+  float *k_scale, *v_scale;  /* device; 8-bit formats only, else NULL */
+} relpos_kv_cache;
+
+typedef struct {
+  relpos_kv_cache cache;     /* written */
+  int32_t B, N;              /* tokens: k, v are [B, kv_heads, N, d] views (packed: as for relpos_rotary) */
+  int32_t dtype;             /* RELPOS_F16 or RELPOS_BF16; equal to the format of a 16-bit cache */
+  int32_t pad;
+  const void *k, *v;         /* device; rows 16-byte aligned (strides multiples of 8 elements) */
+  int64_t k_stride_b, k_stride_h, k_stride_n;
+  int64_t v_stride_b, v_stride_h, v_stride_n;
+  const int64_t* slots;      /* device [B, N]: page x page_size + offset of each token.  A negative
+                                slot, or one past the pool, is skipped (a rejected or padding token).
+                                The slots of one call are distinct: two tokens with the same slot
+                                leave an unspecified mixture of their rows there. */
+} relpos_cache_write_args;
+
+/* Writes the tokens' rows, quantised to the cache's format.  Errors:
+ * INVALID_ARG, UNSUPPORTED (dtype or format), CUDA. */
+int relpos_cache_write(const relpos_cache_write_args* a, relpos_stream_t stream);
+
+typedef struct {
+  relpos_kv_cache cache;     /* read */
+  int32_t B, pages_per_seq;  /* page_table is device int32 [B, pages_per_seq] */
+  int32_t total_tokens;      /* rows of k and v */
+  int32_t dtype;             /* RELPOS_F16 or RELPOS_BF16, whatever the format */
+  const int32_t* page_table;
+  const int32_t* cu_seqlens; /* device int32 [B + 1], non-decreasing: sequence b's tokens 0, 1, ... go to
+                                rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 */
+  void *k, *v;               /* device [total_tokens, kv_heads, d]; rows in front of the first sequence
+                                and behind the last one are left as they were */
+} relpos_cache_read_args;
+
+/* Reads sequences back into the packed variable-length layout (values
+ * code x scale, in fp32, rounded once).  A token whose page lies outside the
+ * table or the pool reads as zeros.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int relpos_cache_read(const relpos_cache_read_args* a, relpos_stream_t stream);
+
+/* --- attention of drafted tokens over the cache ---------------------------- */
+
+typedef struct {
+  relpos_kv_cache cache;     /* read; d 64 or 128; a 16-bit cache has q's type */
+  int32_t B, T, H, pad;      /* T drafted tokens (nodes) of each sequence, 1 .. 64; H a multiple of
+                                kv_heads (query head h reads key head h / (H / kv_heads)); B <= 4096 */
+  int32_t dtype;             /* RELPOS_F16 or RELPOS_BF16: q, k, v, aq */
+  int32_t out_dtype;         /* dtype, or RELPOS_F32 */
+  float tau;                 /* finite and > 0 */
+  int32_t max_seqlen;        /* N of the map (its table rows; offsets are clamped to [1 - N, N - 1]) */
+  int32_t pages_per_seq;     /* page_table is device int32 [B, pages_per_seq]; a token whose page lies
+                                outside the pool is masked */
+  int32_t table_per_head;    /* aq is [H, R, d] (1) or [R, d] (0) */
+  relpos_map_desc map;       /* read when aq or b is given */
+  int32_t mask_per_seq;      /* tree_mask is [B, T] (1) or [T] (0) */
+  const int32_t* page_table;
+  const int32_t* lengths;    /* device [B]: cached tokens; clamped to [0, pages_per_seq page_size] */
+  const int64_t* tree_mask;  /* device: bit u of entry i is set where node i attends node u (itself
+                                among them); an entry 0 is a padding node (O = 0, LSE = -inf); bits from
+                                T on are ignored.  NULL: a chain, node i attends nodes 0 .. i */
+  const void *q;             /* device [B, H, T, d] view */
+  const void *k, *v;         /* device [B, kv_heads, T, d] views: the nodes' own rows, not yet in the cache */
+  int64_t q_stride_b, q_stride_h, q_stride_n;   /* multiples of 8 elements, rows 16-byte aligned */
+  int64_t k_stride_b, k_stride_h, k_stride_n;
+  int64_t v_stride_b, v_stride_h, v_stride_n;
+  const void* aq;            /* device table, or NULL */
+  const float* b;            /* device [H, R], or NULL */
+  void* o;                   /* device [B, H, T, d] out_dtype, contiguous */
+  float* lse;                /* device [B, H, T], natural log */
+} relpos_tree_args;
+
+/* Workspace bytes of relpos_tree_attn (pointers are not read, only whether aq
+ * and b are NULL).  Errors: INVALID_ARG, UNSUPPORTED. */
+int relpos_tree_workspace_size(const relpos_tree_args* a, size_t* bytes);
+
+/* Attention of T drafted tokens over the cache and over one another, with the
+ * unified score of the forward (the aq and b terms):
+ *   S_ij = tau (q_i.k_j + q_i.aQ[phi(p_j - p_i)] + b[phi(p_j - p_i)])
+ * where cached token j has position j, and node u has position
+ * lengths[b] + (set bits of its mask) - 1, its depth in the tree.  T = 1 is
+ * plain decoding.  With the same inputs the result does not depend on what
+ * else runs, and equal calls give equal bits.  workspace: device, 256-byte
+ * aligned, contents ignored; calls that may overlap on the GPU need workspaces
+ * of their own.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+int relpos_tree_attn(const relpos_tree_args* a, void* workspace, size_t ws_bytes, relpos_stream_t stream);
+
 /* --- measurement ---------------------------------------------------------- */
 
 /* Per-phase device time collected between relpos_profile_start and
  * relpos_profile_stop.  Phases: "tables", "projection", "fwd_attention",
  * "bwd_prep", "bwd_dq", "bwd_dkdv", "fold_ranges", "relation_grads",
- * "bwd_attention".  The backward runs its Q-parallel pass (then the query-side
+ * "bwd_attention", "rotary", "cache_write", "cache_read", "tree_relation",
+ * "tree_attention".  The backward runs its Q-parallel pass (then the query-side
  * relation gradients) on the caller's stream and its K-parallel pass (then the
  * key side) concurrently on a second stream, so "bwd_dkdv" and the key-side
  * "relation_grads" are measured on that stream and overlap other phases.
