@@ -855,7 +855,7 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
   p->o = a->o; p->lse = a->lse;
   p->c2 = a->tau * kLog2e;
   const int rows = p->G * a->T;
-  p->rows_per_block = tree_rows_per_block(rows, a->cache.d);
+  p->rows_per_block = tree_rows_per_block(rows);
   p->row_blocks = (rows + p->rows_per_block - 1) / p->rows_per_block;
   if ((long long)a->B * a->cache.kv_heads * p->row_blocks > 0x7fffffffLL) return RELPOS_ERR_INVALID_ARG;
   p->grid = tree_grid(*p);

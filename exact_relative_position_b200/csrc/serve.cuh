@@ -91,9 +91,8 @@ struct TreeParams {
   float* part;
   int grid, rows_per_block, row_blocks;
 };
-// Rows of query (heads times nodes) one block takes, and its resident blocks.
-int tree_rows_per_block(int rows, int d);
-int tree_tile_keys(int rows, int d);
+// Rows of query (heads times nodes) one block takes, and the blocks of a launch.
+int tree_rows_per_block(int rows);
 int tree_grid(const TreeParams& p);
 cudaError_t launch_tree_relation(const TreeParams& p, cudaStream_t s);
 cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s);

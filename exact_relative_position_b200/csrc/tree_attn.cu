@@ -139,10 +139,26 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   }
 }
 
-template <class TL> constexpr int blocks_of(bool wide) {
-  const int b = wide ? stage_bytes<TL, RELPOS_CACHE_F16>() : stage_bytes<TL, RELPOS_CACHE_INT8>();
-  const int fit = (227 * 1024 - 17 * 1024) / (b + 2048);   // 17 KB: the longest list of sequences
-  return fit < 4 ? fit : 4;
+// Keys to a tile and blocks to an SM of the tiling a call takes.
+struct Shape {
+  int tk, bps;
+};
+template <class T>
+Shape shape_rows(int rows_per_block) {
+  switch (rows_per_block) {
+    case 8: return {T::R8::TK, T::R8::BPS};
+    case 16: return {T::R16::TK, T::R16::BPS};
+    case 32: return {T::R32::TK, T::R32::BPS};
+    default: return {T::R64::TK, T::R64::BPS};
+  }
+}
+bool wide_cache(const TreeParams& p) {
+  return p.c.format == RELPOS_CACHE_F16 || p.c.format == RELPOS_CACHE_BF16;
+}
+Shape shape_of(const TreeParams& p) {
+  if (p.c.d == 64)
+    return wide_cache(p) ? shape_rows<Tilings<64, true>>(p.rows_per_block) : shape_rows<Tilings<64, false>>(p.rows_per_block);
+  return wide_cache(p) ? shape_rows<Tilings<128, true>>(p.rows_per_block) : shape_rows<Tilings<128, false>>(p.rows_per_block);
 }
 
 }  // namespace
@@ -150,28 +166,15 @@ template <class TL> constexpr int blocks_of(bool wide) {
 
 using namespace tree;
 
-int tree_rows_per_block(int rows, int d) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
-int tree_tile_keys(int rows, int d) {
-  if (d == 64) return rows <= 16 ? T64_16::TK : rows <= 32 ? T64_32::TK : T64_64::TK;
-  return rows <= 16 ? T128_16::TK : rows <= 32 ? T128_32::TK : T128_64::TK;
-}
+int tree_rows_per_block(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 // One piece of the line of tiles to each block that can be resident; fewer
 // where there are fewer tiles.
 int tree_grid(const TreeParams& p) {
-  const bool wide = p.c.format == RELPOS_CACHE_F16 || p.c.format == RELPOS_CACHE_BF16;
-  int per_sm;
-  if (p.c.d == 64)
-    per_sm = p.rows_per_block == 16 ? blocks_of<T64_16>(wide) : p.rows_per_block == 32 ? blocks_of<T64_32>(wide)
-                                                                                       : blocks_of<T64_64>(wide);
-  else
-    per_sm = p.rows_per_block == 16 ? blocks_of<T128_16>(wide) : p.rows_per_block == 32 ? blocks_of<T128_32>(wide)
-                                                                                        : blocks_of<T128_64>(wide);
-  const int tk = tree_tile_keys(p.rows_per_block, p.c.d);
-  const long long most = (((long long)p.P << p.c.page_shift) + p.T + tk - 1) / tk + 1;
+  const Shape sh = shape_of(p);
+  const long long most = (((long long)p.P << p.c.page_shift) + p.T + sh.tk - 1) / sh.tk + 1;
   const long long tiles = most * p.B * p.c.Hkv * p.row_blocks;
-  return (int)(tiles < 148LL * per_sm ? tiles : 148LL * per_sm);
+  return (int)(tiles < 148LL * sh.bps ? tiles : 148LL * sh.bps);
 }
 
 cudaError_t launch_tree_relation(const TreeParams& p, cudaStream_t s) {
@@ -206,8 +209,7 @@ cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_combine(const TreeParams& p, cudaStream_t s) {
-  const bool wide = p.c.format == RELPOS_CACHE_F16 || p.c.format == RELPOS_CACHE_BF16;
-  combine_kernel<<<p.B * p.c.Hkv * p.row_blocks, 128, 0, s>>>(p, tree_tile_keys(p.rows_per_block, p.c.d), wide);
+  combine_kernel<<<p.B * p.c.Hkv * p.row_blocks, 128, 0, s>>>(p, shape_of(p).tk, wide_cache(p));
   note_launch(1);
   return cudaGetLastError();
 }

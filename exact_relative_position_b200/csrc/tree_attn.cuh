@@ -15,21 +15,27 @@
 // cut by a piece's end leaves partial maxima, sums and outputs in the
 // workspace, which a second kernel joins in the order of the pieces.
 //
-// Tensor work: mma.sync m16n8k16.  Up to 64 rows share each key, so the
-// kernel does at most 2 x 64 multiply-adds for each element it loads and is
-// bound by memory there; 128-row tcgen05 tiles would run mostly empty.
+// Tensor work: mma.sync m16n8k16 with the keys as the 16 rows and the query
+// rows as the 8 columns, S^T = K Q^T and O^T = V^T P^T, so that decoding with
+// up to eight query heads to a key head fills the tile.  With so few rows each
+// loaded element feeds few multiply-adds and the kernel is bound by memory;
+// 128-row tcgen05 tiles would run mostly empty.
 //
-// Order of the operands.  An MMA sums over k in any order, and names its
-// columns in any order, as long as both operands agree.  Each lane of a quad
-// therefore takes 16 consecutive bytes of a key row for its k slots (one
-// shared-memory load feeds 2 to 4 MMAs, 8-bit codes are expanded in
-// registers), and column slot c of the two 8-key column tiles of 16 keys
-// stands for key 4 (c / 2) + c % 2 (+ 2 in the second), which makes a lane's
-// four score columns, and so its four rows of V, consecutive keys.
+// Order of the operands.  An MMA sums over k in any order and names its rows in
+// any order, as long as both operands agree.  Each lane of a quad therefore
+// takes 16 consecutive bytes of a key row for its k slots (one shared-memory
+// load feeds 2 to 4 MMAs, 8-bit codes are expanded in registers), and row slot
+// c of 16 keys stands for key 4 (c / 2) + c % 2 (c < 8) or 2 more than slot c - 8,
+// which makes the four rows of V that a lane pairs up consecutive keys.  P^T
+// goes from the score layout to the operand layout by movmatrix.
+//
+// The row maximum is moved only when a score exceeds it by 2^8: weights stay
+// within 2^8, far from fp16's range, and most steps skip the rescaling of O and
+// the reduction over lanes.
 //
 // 8-bit caches: codes are exact in fp16.  The scale of key j multiplies its
-// score column; that of its value row is folded into the exponent, so that
-// the fp16 weight is 2^(s_ij + log2 sv_j - m_i) <= 1 with m_i the row's
+// score row; that of its value row is folded into the exponent, so that
+// the fp16 weight is 2^(s_ij + log2 sv_j - m_i) with m_i the row's
 // running maximum of that sum, and the softmax sum divides it out in fp32:
 //   P'_ij = 2^(s_ij + log2 sv_j - m_i),  l_i = sum_j P'_ij / sv_j,
 //   O_i = sum_j P'_ij code_j / l_i,      LSE_i = m_i + log2 l_i (base 2).
@@ -51,11 +57,11 @@ namespace tree {
 
 constexpr float kMinLogScale = -100.f;   // value scales count as at least 2^-100: l stays finite
 
-// Tiling of a row count: WM x WN warps, MT 16-row tiles to a warp, KW keys to
-// a warp and step.
-template <int D_, int WM_, int WN_, int MT_, int KW_, int STAGES_> struct Tiling {
-  static constexpr int D = D_, WM = WM_, WN = WN_, MT = MT_, KW = KW_, STAGES = STAGES_;
-  static constexpr int ROWS = WM * MT * 16, TK = WN * KW;
+// Tiling of a row count: WM x WN warps, NR tiles of 8 query rows to a warp, KW
+// keys to a group of WM warps and stage, SK keys to a step, BPS blocks to an SM.
+template <int D_, int WM_, int WN_, int NR_, int KW_, int SK_, int STAGES_, int BPS_> struct Tiling {
+  static constexpr int D = D_, WM = WM_, WN = WN_, NR = NR_, KW = KW_, SK = SK_, STAGES = STAGES_, BPS = BPS_;
+  static constexpr int ROWS = WM * NR * 8, TK = WN * KW;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -153,6 +159,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -209,13 +220,6 @@ __device__ __forceinline__ uint32_t clean2(uint32_t w, bool& seen) {
   return (lo ? 0u : w & 0xffffu) | (hi ? 0u : w & 0xffff0000u);
 }
 
-struct RowInfo {
-  int t, h;                      // node and query head; t < 0: no such row
-  int depth;
-  unsigned long long mask;
-  const float* z;                // its relation terms at offset 0 - e_lo ... (null: none)
-};
-
 __device__ __forceinline__ unsigned long long node_mask(const TreeParams& p, int b, int t) {
   const unsigned long long live = p.T == 64 ? ~0ull : (1ull << p.T) - 1;
   const unsigned long long m = p.mask ? (unsigned long long)p.mask[(long long)b * p.mask_bs + t]
@@ -247,18 +251,25 @@ __device__ __forceinline__ void store_row(const TreeParams& p, int b, int hkv, i
 }
 
 // ---------------------------------------------------------------- the kernel
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 template <class TL, typename QT, int FMT>
-__global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr bool WIDE = FMT == RELPOS_CACHE_F16;        // the cache has the queries' 16-bit type
-  constexpr int D = TL::D, WM = TL::WM, WN = TL::WN, MT = TL::MT, KW = TL::KW, TK = TL::TK, ROWS = TL::ROWS;
+  constexpr int D = TL::D, WM = TL::WM, WN = TL::WN, NR = TL::NR, KW = TL::KW, TK = TL::TK, ROWS = TL::ROWS;
   constexpr int ES = WIDE ? 2 : 1;
   constexpr int CPR = D * ES / 16;                      // chunks of a row
   constexpr int GT = WM * 32;                           // threads that share a group of KW keys
   constexpr int KS = D / 16;                            // k steps of q.k
-  constexpr int NT = D / 8;                             // column tiles of the output
-  constexpr int SG = KW / 16;                           // groups of 16 keys
+  constexpr int MTD = D / 16;                           // 16-row tiles of the output's d
+  constexpr int SG = TL::SK / 16;                       // groups of 16 keys to a step
   constexpr int HALF = KW * CPR * 16;                   // bytes of a group's keys (or values) in a stage
   constexpr int GSTAGE = 2 * HALF + (WIDE ? 0 : KW * 8);
+  constexpr int MP = D + 4;                             // pitch of the rows that the warps join
   using MT16 = typename std::conditional<WIDE, QT, __half>::type;   // operand type of the MMAs
 
   extern __shared__ __align__(128) uint8_t smem[];
@@ -268,11 +279,12 @@ __global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeP
   int* pre = reinterpret_cast<int*>(smem);              // [B + 1], rounded up to 128 bytes
   const uint32_t pre_bytes = (uint32_t)((p.B + 1) * 4 + 127) & ~127u;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wm = warp / WN, wn = warp % WN;             // WN == 4: wm = 0
+  const int wm = warp / WN, wn = warp % WN;
   const int gtid = wm * 32 + lane;                      // place in the group of warps with this wn
   const int q4 = lane & 3, r8 = lane >> 2;
+  const int key0 = 4 * (r8 >> 1) + (r8 & 1);            // key (of 16) of row slot r8; slot r8 + 8: two more
   const uint32_t stage0 = smem_u32(smem) + pre_bytes + (uint32_t)(wn * TL::STAGES * GSTAGE);
-  float* merge = reinterpret_cast<float*>(smem + pre_bytes);   // [WN][ROWS][D], over the stages
+  float* merge = reinterpret_cast<float*>(smem + pre_bytes);   // [WN][ROWS][MP], over the stages
 
   auto group_sync = [&]() {
     if (WM == 1) __syncwarp();
@@ -300,79 +312,6 @@ __global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeP
     const int tile1 = (int)min((long long)nt, tile0 + (my_end - cur));
     const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
     const int len = seq_len(p, b);
-
-    // rows of this thread: MT tiles, rows r8 and r8 + 8 of each
-    RowInfo row[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = rb * ROWS + (wm * MT + mt) * 16 + r8 + 8 * e;
-        RowInfo& x = row[mt][e];
-        x.t = -1;
-        x.h = 0;
-        x.depth = 0;
-        x.mask = 0;
-        x.z = nullptr;
-        if (r < R) {
-          x.t = r / p.G;
-          x.h = hkv * p.G + (r - x.t * p.G);
-          x.mask = node_mask(p, b, x.t);
-          x.depth = max(__popcll(x.mask) - 1, 0);
-          if (p.z) x.z = p.z + b * p.z_b + x.h * p.z_h + x.t * p.z_t;
-        }
-      }
-
-    // ---- queries: A fragments in the permuted k order
-    uint32_t qa[MT][KS][4];
-    uint32_t top = 0;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const RowInfo& x = row[mt][e];
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + b * p.qs.b + x.h * p.qs.h + (long long)x.t * p.qs.n;
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
-          // 16-bit keys: 8 elements at 32 u + 8 q; 8-bit keys: 8 of the 16 elements at 64 (u / 2) + 16 q
-          const int d0 = WIDE ? 32 * u + 8 * q4 : 64 * (u / 2) + 16 * q4 + 8 * (u % 2);
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (x.t >= 0) w = __ldg(reinterpret_cast<const uint4*>(src + d0));
-          qa[mt][2 * u][e] = w.x;
-          qa[mt][2 * u][2 + e] = w.y;
-          qa[mt][2 * u + 1][e] = w.z;
-          qa[mt][2 * u + 1][2 + e] = w.w;
-          if (!WIDE && sizeof(QT) == 2 && DT<QT>::kCoarse)
-            top = amax2(amax2(amax2(amax2(top, w.x), w.y), w.z), w.w);
-        }
-      }
-    float qf = 1.f;                                     // the queries' power of two (8-bit caches)
-    if (!WIDE && DT<QT>::kCoarse) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = exp_of(top);
-      qf = pow2i(e);
-      const float down = pow2i(-e);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) qa[mt][ks][i] = to_half2<QT>(qa[mt][ks][i], down);
-    }
-    const float kc = p.c2 * qf;                         // scores of 8-bit keys: acc * scale_j * kc (base 2)
-
-    float oacc[MT][NT][4];
-    float mrow[MT][2], lrow[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) oacc[mt][n][i] = 0.f;
-      mrow[mt][0] = mrow[mt][1] = -INFINITY;
-      lrow[mt][0] = lrow[mt][1] = 0.f;
-    }
 
     // ---- loads: rows of the cache by page, nodes behind them (16-bit cache)
     const uint8_t* kc_base = static_cast<const uint8_t*>(p.c.k);
@@ -434,35 +373,102 @@ __global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeP
       }
     };
 
-    // online softmax and P V of one group of scores: s[mt][2 g + j][..], base-2
-    // exponents after `p.c2` (16-bit caches) or as they are (8-bit)
-    auto new_max = [&](float (&s)[MT][2 * SG][4]) {
+    uint32_t at_next[LR];
+    {
+      uint32_t at[TL::STAGES - 1][LR];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int s = 0; s < TL::STAGES - 1; ++s) lookup(tile0 + s, at[s]);
+      lookup(tile0 + TL::STAGES - 1, at_next);
+#pragma unroll
+      for (int s = 0; s < TL::STAGES - 1; ++s) {
+        if (tile0 + s < tile1) issue(tile0 + s, s, at[s]);
+        cp_async_commit();
+      }
+    }
+
+    // ---- queries: B fragments in the permuted k order, row r8 of each tile
+    uint32_t qb[NR][KS][2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int r = rb * ROWS + (wm * NR + n) * 8 + r8;
+      const int t = r < R ? r / p.G : 0, h = hkv * p.G + (r < R ? r - t * p.G : 0);
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + b * p.qs.b + h * p.qs.h + (long long)t * p.qs.n;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        // 16-bit keys: 8 elements at 32 u + 8 q; 8-bit keys: 8 of the 16 elements at 64 (u / 2) + 16 q
+        const int d0 = WIDE ? 32 * u + 8 * q4 : 64 * (u / 2) + 16 * q4 + 8 * (u % 2);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < R) w = __ldg(reinterpret_cast<const uint4*>(src + d0));
+        qb[n][2 * u][0] = w.x;
+        qb[n][2 * u][1] = w.y;
+        qb[n][2 * u + 1][0] = w.z;
+        qb[n][2 * u + 1][1] = w.w;
+        if (!WIDE && DT<QT>::kCoarse) top = amax2(amax2(amax2(amax2(top, w.x), w.y), w.z), w.w);
+      }
+    }
+    float qf = 1.f;                                     // the queries' power of two (8-bit caches)
+    if (!WIDE && DT<QT>::kCoarse) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = exp_of(top);
+      qf = pow2i(e);
+      const float down = pow2i(-e);
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qb[n][ks][i] = to_half2<QT>(qb[n][ks][i], down);
+    }
+    const float kc = p.c2 * qf;                         // scores of 8-bit keys: acc * scale_j * kc (base 2)
+
+    // ---- rows 2 q and 2 q + 1 of each tile: their relation terms
+    auto row_of = [&](int n, int e) { return rb * ROWS + (wm * NR + n) * 8 + 2 * q4 + e; };
+    auto z_of = [&](int n, int e) -> const float* {     // at offset e_lo; any row's for a row that is none
+      const int r = min(row_of(n, e), R - 1), t = r / p.G, h = hkv * p.G + (r - t * p.G);
+      return p.z + b * p.z_b + h * p.z_h + t * p.z_t;
+    };
+    float zlow[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) zlow[n][e] = p.z ? z_of(n, e)[0] : 0.f;
+
+    float oacc[NR][MTD][4];
+    float mrow[NR][2], lrow[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int i = 0; i < MTD; ++i) oacc[n][i][0] = oacc[n][i][1] = oacc[n][i][2] = oacc[n][i][3] = 0.f;
+      mrow[n][0] = mrow[n][1] = -INFINITY;
+      lrow[n][0] = lrow[n][1] = 0.f;
+    }
+    const float unit = WIDE ? p.c2 : 1.f;               // base-2 units of scores and maxima
+    const float slack = WIDE ? 8.f / p.c2 : 8.f;
+
+    // moves the maxima where a score exceeds its row's by more than the slack
+    auto new_max = [&](const float (&lm)[NR][2]) {
+      bool up = false;
+#pragma unroll
+      for (int n = 0; n < NR; ++n) up = up || lm[n][0] > mrow[n][0] + slack || lm[n][1] > mrow[n][1] + slack;
+      if (!__any_sync(0xffffffffu, up)) return;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float m = mrow[mt][e];
+          float m = fmaxf(lm[n][e], mrow[n][e]);
 #pragma unroll
-          for (int n = 0; n < 2 * SG; ++n) m = fmaxf(m, fmaxf(s[mt][n][2 * e], s[mt][n][2 * e + 1]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          if (m != mrow[mt][e]) {                       // the quad's lanes agree
-            const float f = ex2((mrow[mt][e] - m) * (WIDE ? p.c2 : 1.f));   // 2^-inf = 0 at the first keys
-            lrow[mt][e] *= f;
+          for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const float f = m == mrow[n][e] ? 1.f : ex2((mrow[n][e] - m) * unit);   // 2^-inf = 0 at the first keys
+          mrow[n][e] = m;
+          lrow[n][e] *= f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              oacc[mt][n][2 * e] *= f;
-              oacc[mt][n][2 * e + 1] *= f;
-            }
-            mrow[mt][e] = m;
+          for (int i = 0; i < MTD; ++i) {
+            oacc[n][i][e] *= f;
+            oacc[n][i][2 + e] *= f;
           }
         }
-    };
-
-    // relation terms of four consecutive offsets from d0 on
-    auto z4 = [&](const float* z, int d0, float (&out)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) out[i] = z[iclamp(d0 + i, p.e_lo, p.e_hi) - p.e_lo];
     };
 
     // adds the non-finite value elements of nodes [ua, ub) to the rows that attend them
@@ -470,217 +476,185 @@ __global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeP
       for (int u = max(ua, 0); u < min(ub, p.T); ++u) {
         const QT* src = static_cast<const QT*>(p.v) + b * p.vs.b + hkv * p.vs.h + u * p.vs.n;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < MTD; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float x = DT<QT>::to_f(src[WIDE ? n * 8 + 2 * q4 + c : (2 * q4 + c) * NT + n]);
+            const float x = DT<QT>::to_f(src[WIDE ? 16 * i + 8 * c + r8 : r8 * (D / 8) + 2 * i + c]);
             if (fabsf(x) <= 3.4028235e38f) continue;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if ((row[mt][e].mask >> u) & 1ull) oacc[mt][n][2 * e + c] += x;
+              for (int e = 0; e < 2; ++e) {
+                const int r = row_of(n, e);
+                if (r < R && ((node_mask(p, b, r / p.G) >> u) & 1ull)) oacc[n][i][2 * c + e] += x;
+              }
           }
       }
     };
 
-    uint32_t at_next[LR];
-    {
-      uint32_t at[LR];
+    // One step of SK keys from key ko of the group's KW, staged at sk / sv.  EASY: every
+    // key is a valid cached one, and its relation term saturated (or there is none).
+    auto step = [&](auto easy, int k0, int ko, uint32_t sk, uint32_t sv, int stage) {
+      constexpr bool EASY = decltype(easy)::value;
+      float s[NR][SG][4];
 #pragma unroll
-      for (int s = 0; s < TL::STAGES - 1; ++s) {
-        lookup(tile0 + s, at);
-        if (tile0 + s < tile1) issue(tile0 + s, s, at);
-        cp_async_commit();
-      }
-      lookup(tile0 + TL::STAGES - 1, at_next);
-    }
-    int stage = 0;
-    for (int tile = tile0; tile < tile1; ++tile) {
-      cp_async_wait<TL::STAGES - 2>();
-      group_sync();
-      {
-        const int nx = tile + TL::STAGES - 1;
-        int ns = stage + TL::STAGES - 1;
-        if (ns >= TL::STAGES) ns -= TL::STAGES;
-        if (nx < tile1) issue(nx, ns, at_next);
-        cp_async_commit();
-        lookup(nx + 1, at_next);
-      }
-      const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
-      const int k0 = tile * TK + wn * KW;
-      bool full = true;
-#pragma unroll
-      for (int i = 0; i < LR; ++i)
-        full = full && valid_bits[wn][stage][i] == (KW >= 32 ? 0xffffffffu : (1u << (KW & 31)) - 1u);
-      const bool plain = full && k0 + KW <= len;        // every key is a valid cached one
-
-      // ---- scores
-      float s[MT][2 * SG][4];
-      const bool low = k0 + KW <= len && k0 + KW - 1 - len <= p.e_lo;   // every offset is saturated: one value a row
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int g = 0; g < SG; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][g][i] = WIDE && EASY ? zlow[n][i & 1] : 0.f;
+      float z[NR][SG][4];
+      if (!EASY && p.z) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float z[4] = {0.f, 0.f, 0.f, 0.f};
-            if (WIDE && p.z && row[mt][e].z) {
-              if (low) {
-                z[0] = z[1] = z[2] = z[3] = row[mt][e].z[0];
-              } else {
-                const int j = k0 + 16 * g + 4 * q4, here = len + row[mt][e].depth;
-                z4(row[mt][e].z, j - here, z);
-                if (j + 4 > len) {
+            const float* zr = z_of(n, e);
+            const int r = min(row_of(n, e), R - 1);
+            const int depth = max(__popcll(node_mask(p, b, r / p.G)) - 1, 0);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const int u = j + i - len;
-                    if (u >= 0 && u < p.T) {
-                      const int du = max(__popcll(node_mask(p, b, u)) - 1, 0);
-                      z[i] = row[mt][e].z[iclamp(du - row[mt][e].depth, p.e_lo, p.e_hi) - p.e_lo];
-                    }
-                  }
-                }
+            for (int g = 0; g < SG; ++g)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                int at = k0 + ko + 16 * g + key0 + 2 * j - len;
+                if (WIDE && at >= 0) at = at < p.T ? max(__popcll(node_mask(p, b, at)) - 1, 0) : 0;
+                const float x = zr[iclamp(at - depth, p.e_lo, p.e_hi) - p.e_lo];
+                if (WIDE) s[n][g][2 * j + e] = x;
+                else z[n][g][2 * j + e] = x;
               }
-            }
-            s[mt][2 * g][2 * e] = z[0];
-            s[mt][2 * g][2 * e + 1] = z[1];
-            s[mt][2 * g + 1][2 * e] = z[2];
-            s[mt][2 * g + 1][2 * e + 1] = z[3];
           }
+      }
+      // ---- scores: k steps outside, so that consecutive MMAs have their own sums
 #pragma unroll
-      for (int g = 0; g < SG; ++g)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int kr = 16 * g + 4 * (r8 >> 1) + (r8 & 1) + 2 * j;
-#pragma unroll
-          for (int u = 0; u < CPR / 4; ++u) {
-            const uint4 w = lds128(sk + chunk_at<CPR, WIDE, false>(kr, 4 * u + q4));
-            if (WIDE) {
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                MmaOp<MT16>::run(s[mt][2 * g + j], qa[mt][2 * u], w.x, w.y);
-                MmaOp<MT16>::run(s[mt][2 * g + j], qa[mt][2 * u + 1], w.z, w.w);
-              }
-            } else {
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t b0, b1;
-                expand4<FMT>(ww[i], b0, b1);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) MmaOp<MT16>::run(s[mt][2 * g + j], qa[mt][(4 * u + i) % KS], b0, b1);
-              }
-            }
-          }
-        }
-      float rsv[SG][4];                                 // 1 / value scale of the thread's keys
-      if (!WIDE) {
+      for (int u = 0; u < CPR / 4; ++u) {
 #pragma unroll
         for (int g = 0; g < SG; ++g) {
-          const uint4 a = lds128(sk + 2 * HALF + (16 * g + 4 * q4) * 4);
-          const uint4 v4 = lds128(sk + 2 * HALF + KW * 4 + (16 * g + 4 * q4) * 4);
-          const float kcol[4] = {__uint_as_float(a.x) * kc, __uint_as_float(a.y) * kc, __uint_as_float(a.z) * kc,
-                                 __uint_as_float(a.w) * kc};
-          const float vs4[4] = {__uint_as_float(v4.x), __uint_as_float(v4.y), __uint_as_float(v4.z),
-                                __uint_as_float(v4.w)};
-          float lg[4];
+          const int kr = ko + 16 * g + key0;
+          const uint4 w0 = lds128(sk + chunk_at<CPR, WIDE, false>(kr, 4 * u + q4));
+          const uint4 w1 = lds128(sk + chunk_at<CPR, WIDE, false>(kr + 2, 4 * u + q4));
+          if (WIDE) {
+            const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // not fmaxf, which would drop the NaN of a spoilt row
-            const float v = vs4[i] < 0x1p-100f ? 0x1p-100f : vs4[i];
-            lg[i] = lg2(v);
-            rsv[g][i] = rcp(v);
-          }
+            for (int n = 0; n < NR; ++n) MmaOp<MT16>::run(s[n][g], a0, qb[n][2 * u][0], qb[n][2 * u][1]);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+            for (int n = 0; n < NR; ++n) MmaOp<MT16>::run(s[n][g], a1, qb[n][2 * u + 1][0], qb[n][2 * u + 1][1]);
+          } else {
+            const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float z[4] = {0.f, 0.f, 0.f, 0.f};
-              if (p.z && row[mt][e].z) {
-                if (low) z[0] = z[1] = z[2] = z[3] = row[mt][e].z[0];
-                else z4(row[mt][e].z, k0 + 16 * g + 4 * q4 - len - row[mt][e].depth, z);
-              }
+            for (int i = 0; i < 4; ++i) {
+              uint32_t a[4];
+              expand4<FMT>(x0[i], a[0], a[2]);
+              expand4<FMT>(x1[i], a[1], a[3]);
+              const int ks = (4 * u + i) % KS;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float& x = s[mt][2 * g + (i >> 1)][2 * e + (i & 1)];
-                x = fmaf(x, kcol[i], lg[i] + z[i]);
-              }
+              for (int n = 0; n < NR; ++n) MmaOp<MT16>::run(s[n][g], a, qb[n][ks][0], qb[n][ks][1]);
             }
+          }
         }
       }
-      if (!plain) {
+      float rsv[SG][2];                                 // 1 / value scale of the thread's keys
+      if (!WIDE) {
 #pragma unroll
         for (int g = 0; g < SG; ++g)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kl = 16 * g + 4 * q4 + i;
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a = sk + 2 * HALF + (ko + 16 * g + key0 + 2 * j) * 4;
+            const float kcol = __uint_as_float(lds32(a)) * kc;
+            float v = __uint_as_float(lds32(a + KW * 4));
+            v = v < 0x1p-100f ? 0x1p-100f : v;          // not fmaxf, which would drop the NaN of a spoilt row
+            const float lg = lg2(v);
+            rsv[g][j] = rcp(v);
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& x = s[n][g][2 * j + e];
+                if (EASY) x = fmaf(x, kcol, lg + zlow[n][e]);
+                else x = fmaf(x, kcol, p.z ? lg + z[n][g][2 * j + e] : lg);
+              }
+          }
+      }
+      if (!EASY) {
+#pragma unroll
+        for (int g = 0; g < SG; ++g)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int kl = ko + 16 * g + key0 + 2 * j;
             const bool there = (valid_bits[wn][stage][kl >> 5] >> (kl & 31)) & 1u;
             const int u = k0 + kl - len;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const bool keep = there && (u < 0 || ((row[mt][e].mask >> (u & 63)) & 1ull));
-                if (!keep) s[mt][2 * g + (i >> 1)][2 * e + (i & 1)] = -INFINITY;
+                bool keep = there;
+                if (WIDE && there && u >= 0) {
+                  const int r = row_of(n, e);
+                  keep = r < R && ((node_mask(p, b, r / p.G) >> u) & 1ull);
+                }
+                if (!keep) s[n][g][2 * j + e] = -INFINITY;
               }
           }
       }
       // ---- softmax
-      new_max(s);
-      uint32_t pa[MT][SG][4];
+      float lm[NR][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float m0 = safe(mrow[mt][e]);
+          lm[n][e] = fmaxf(s[n][0][e], s[n][0][2 + e]);
 #pragma unroll
-          for (int g = 0; g < SG; ++g) {
-            float w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = s[mt][2 * g + (i >> 1)][2 * e + (i & 1)];
-              w[i] = WIDE ? ex2(fmaf(x, p.c2, -m0 * p.c2)) : ex2(x - m0);
-              lrow[mt][e] = WIDE ? lrow[mt][e] + w[i] : fmaf(w[i], rsv[g][i], lrow[mt][e]);
-            }
-            pa[mt][g][e] = DT<MT16>::pack(w[0], w[1]);
-            pa[mt][g][2 + e] = DT<MT16>::pack(w[2], w[3]);
-          }
+          for (int g = 1; g < SG; ++g) lm[n][e] = fmaxf(lm[n][e], fmaxf(s[n][g][e], s[n][g][2 + e]));
         }
-      // ---- P V
+      new_max(lm);
+      uint32_t pb[NR][SG][2];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float m0 = safe(mrow[n][0]) * unit, m1 = safe(mrow[n][1]) * unit;
+#pragma unroll
+        for (int g = 0; g < SG; ++g)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float w0 = ex2(WIDE ? fmaf(s[n][g][2 * j], p.c2, -m0) : s[n][g][2 * j] - m0);
+            const float w1 = ex2(WIDE ? fmaf(s[n][g][2 * j + 1], p.c2, -m1) : s[n][g][2 * j + 1] - m1);
+            lrow[n][0] = WIDE ? lrow[n][0] + w0 : fmaf(w0, rsv[g][j], lrow[n][0]);
+            lrow[n][1] = WIDE ? lrow[n][1] + w1 : fmaf(w1, rsv[g][j], lrow[n][1]);
+            pb[n][g][j] = transpose8(DT<MT16>::pack(w0, w1));
+          }
+      }
+      // ---- O^T += V^T P^T
       bool odd = false;                                 // a node's value element is not finite
 #pragma unroll
       for (int g = 0; g < SG; ++g) {
         if (WIDE) {
-          const int mi = lane >> 3, n = lane & 7;
-          const int kr = 16 * g + 4 * (n >> 1) + (n & 1) + 2 * (mi & 1);
+          const int mi = lane >> 3, c = lane & 7;       // this lane's row address: slot c of matrix mi
+          const int kr = ko + 16 * g + 4 * (c >> 1) + (c & 1) + 2 * (mi >> 1);
 #pragma unroll
-          for (int dp = 0; dp < NT / 2; ++dp) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(sv + chunk_at<CPR, WIDE, true>(kr, dp * 2 + (mi >> 1)), b0, b1, b2, b3);
-            if (k0 + 16 * g + 16 > len) {               // some of these 16 keys are nodes
-              const int kn = k0 + 16 * g + 4 * q4 - len;   // node of this lane's first key (b0: +0, +1; b1: +2, +3)
-              bool x0 = false, x1 = false;
-              const uint32_t n0 = clean2<QT>(b0, x0), n2 = clean2<QT>(b2, x0);
-              const uint32_t n1 = clean2<QT>(b1, x1), n3 = clean2<QT>(b3, x1);
-              // a pair that holds a cached key stays as it is where that key's element is the odd one
-              if (x0 && kn + 1 >= 0) { b0 = kn >= 0 ? n0 : (n0 & 0xffff0000u) | (b0 & 0xffffu);
-                                       b2 = kn >= 0 ? n2 : (n2 & 0xffff0000u) | (b2 & 0xffffu); odd = true; }
-              if (x1 && kn + 3 >= 0) { b1 = kn + 2 >= 0 ? n1 : (n1 & 0xffff0000u) | (b1 & 0xffffu);
-                                       b3 = kn + 2 >= 0 ? n3 : (n3 & 0xffff0000u) | (b3 & 0xffffu); odd = true; }
+          for (int i = 0; i < MTD; ++i) {
+            uint32_t a[4];
+            ldsm_x4_t(sv + chunk_at<CPR, WIDE, true>(kr, 2 * i + (mi & 1)), a[0], a[1], a[2], a[3]);
+            if (!EASY && k0 + ko + 16 * g + 16 > len) { // some of these 16 keys are nodes
+              const int kn = k0 + ko + 16 * g + 4 * q4 - len;   // node of this lane's first key (a0, a1: +0, +1; a2, a3: +2, +3)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int first = kn + (x >= 2 ? 2 : 0);
+                bool seen = false;
+                const uint32_t clean = clean2<QT>(a[x], seen);
+                // a cached key's element stays as it is
+                if (seen && first + 1 >= 0) {
+                  a[x] = first >= 0 ? clean : (clean & 0xffff0000u) | (a[x] & 0xffffu);
+                  odd = true;
+                }
+              }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              MmaOp<MT16>::run(oacc[mt][2 * dp], pa[mt][g], b0, b1);
-              MmaOp<MT16>::run(oacc[mt][2 * dp + 1], pa[mt][g], b2, b3);
-            }
+            for (int n = 0; n < NR; ++n) MmaOp<MT16>::run(oacc[n][i], a, pb[n][g][0], pb[n][g][1]);
           }
         } else {
           // D / 8 consecutive columns of four consecutive keys
           uint32_t vw[4][D / 32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int kr = 16 * g + 4 * q4 + i;
+            const int kr = ko + 16 * g + 4 * q4 + i;
             if (D == 128) {
               const uint4 w = lds128(sv + chunk_at<CPR, WIDE, true>(kr, r8));
               vw[i][0] = w.x;
@@ -694,20 +668,47 @@ __global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeP
             }
           }
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            uint32_t b0[4], b1[4];
-            expand4<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x5140), b0[0], b0[1]);
-            expand4<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x7362), b0[2], b0[3]);
-            expand4<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x5140), b1[0], b1[1]);
-            expand4<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x7362), b1[2], b1[3]);
+          for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c) {
+              uint32_t a[4];
+              expand4<FMT>(__byte_perm(vw[0][w], vw[1][w], c ? 0x7362 : 0x5140), a[0], a[1]);
+              expand4<FMT>(__byte_perm(vw[2][w], vw[3][w], c ? 0x7362 : 0x5140), a[2], a[3]);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) MmaOp<MT16>::run(oacc[mt][4 * w + c], pa[mt][g], b0[c], b1[c]);
-          }
+              for (int n = 0; n < NR; ++n) MmaOp<MT16>::run(oacc[n][2 * w + c], a, pb[n][g][0], pb[n][g][1]);
+            }
         }
       }
-      if (WIDE && k0 + KW > len && __any_sync(0xffffffffu, odd)) add_non_finite(k0 - len, k0 + KW - len);
+      if (WIDE && !EASY && __any_sync(0xffffffffu, odd)) add_non_finite(k0 + ko - len, k0 + ko + TL::SK - len);
+    };
+
+    int stage = 0;
+#pragma unroll 1
+    for (int tile = tile0; tile < tile1; ++tile) {
+      cp_async_wait<TL::STAGES - 2>();
+      group_sync();
+      {
+        const int nx = tile + TL::STAGES - 1;
+        int ns = stage + TL::STAGES - 1;
+        if (ns >= TL::STAGES) ns -= TL::STAGES;
+        if (nx < tile1) issue(nx, ns, at_next);
+        cp_async_commit();
+        lookup(nx + 1, at_next);
+      }
+      const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
+      const int k0 = tile * TK + wn * KW;
+      bool easy = k0 + KW <= len && (!p.z || k0 + KW - 1 - len <= p.e_lo);
+#pragma unroll
+      for (int i = 0; i < LR; ++i)
+        easy = easy && valid_bits[wn][stage][i] == (KW >= 32 ? 0xffffffffu : (1u << (KW & 31)) - 1u);
+      if (easy) {
+#pragma unroll 1
+        for (int ko = 0; ko < KW; ko += TL::SK) step(std::true_type{}, k0, ko, sk, sv, stage);
+      } else {
+#pragma unroll 1
+        for (int ko = 0; ko < KW; ko += TL::SK)
+          if (k0 + ko < len + (WIDE ? p.T : 0)) step(std::false_type{}, k0, ko, sk, sv, stage);
+      }
       if (++stage == TL::STAGES) stage = 0;
     }
     cp_async_wait<0>();
@@ -716,165 +717,156 @@ __global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeP
     // 16 nodes at a time; bf16 rows enter as fp16 times a power of two that
     // takes the place of the scale
     if (!WIDE && tile1 == nt) {
+#pragma unroll 1
       for (int u0 = 16 * wn; u0 < p.T; u0 += 16 * WN) {
-        float s[MT][2 * SG][4];
+        float s[NR][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        const uint16_t* kn = static_cast<const uint16_t*>(p.k) + b * p.ks.b + hkv * p.ks.h;
+        const uint16_t* vn = static_cast<const uint16_t*>(p.v) + b * p.vs.b + hkv * p.vs.h;
+        auto part = [&](const uint16_t* base, long long stride, int u, int d0) {
+          return u < p.T ? __ldg(reinterpret_cast<const uint4*>(base + u * stride + d0)) : make_uint4(0, 0, 0, 0);
+        };
+        float down[2] = {1.f, 1.f}, kcol[2] = {kc, kc};
+        if (DT<QT>::kCoarse) {
 #pragma unroll
-          for (int n = 0; n < 2 * SG; ++n)
+          for (int j = 0; j < 2; ++j) {
+            uint32_t kt = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][n][i] = n < 2 ? 0.f : -INFINITY;
-        float kmul[2];
-        bool odd = false;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int u = u0 + 4 * (r8 >> 1) + (r8 & 1) + 2 * j;
-          uint32_t kw[D / 8];
-          uint32_t kt = 0;
-#pragma unroll
-          for (int w = 0; w < D / 64; ++w)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (u < p.T)
-                x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k) + b * p.ks.b + hkv * p.ks.h +
-                                                         u * p.ks.n + 64 * w + 16 * q4 + 8 * hh));
-              kw[8 * w + 4 * hh] = x.x;
-              kw[8 * w + 4 * hh + 1] = x.y;
-              kw[8 * w + 4 * hh + 2] = x.z;
-              kw[8 * w + 4 * hh + 3] = x.w;
-              if (DT<QT>::kCoarse) kt = amax2(amax2(amax2(amax2(kt, x.x), x.y), x.z), x.w);
+            for (int w = 0; w < D / 32; ++w) {
+              const uint4 x = part(kn, p.ks.n, u0 + key0 + 2 * j, 64 * (w / 2) + 16 * q4 + 8 * (w % 2));
+              kt = amax2(amax2(amax2(amax2(kt, x.x), x.y), x.z), x.w);
             }
-          float down = 1.f;
-          kmul[j] = 1.f;
-          if (DT<QT>::kCoarse) {
             kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, 1));
             kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, 2));
             const int e = exp_of(kt);
-            down = pow2i(-e);
-            kmul[j] = pow2i(e);
-          }
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint32_t b0 = to_half2<QT>(kw[2 * ks], down), b1 = to_half2<QT>(kw[2 * ks + 1], down);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) MmaOp<MT16>::run(s[mt][j], qa[mt][ks], b0, b1);
+            down[j] = pow2i(-e);
+            kcol[j] = pow2i(e) * kc;
           }
         }
-        // the power of key slot c lives in the lanes with r8 = c: columns 2 q and 2 q + 1 of this lane
-        float kcol[4], lg[4], rv[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int w = 0; w < D / 32; ++w) {
+          const int d0 = 64 * (w / 2) + 16 * q4 + 8 * (w % 2);
+          const uint4 x0 = part(kn, p.ks.n, u0 + key0, d0), x1 = part(kn, p.ks.n, u0 + key0 + 2, d0);
+          const uint32_t a0[4] = {to_half2<QT>(x0.x, down[0]), to_half2<QT>(x1.x, down[1]), to_half2<QT>(x0.y, down[0]),
+                                  to_half2<QT>(x1.y, down[1])};
+          const uint32_t a1[4] = {to_half2<QT>(x0.z, down[0]), to_half2<QT>(x1.z, down[1]), to_half2<QT>(x0.w, down[0]),
+                                  to_half2<QT>(x1.w, down[1])};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) kcol[2 * j + c] = __shfl_sync(0xffffffffu, kmul[j], 4 * (2 * q4 + c)) * kc;
-        uint32_t vh[4][D / 16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int u = u0 + 4 * q4 + i;
-          uint32_t vt = 0;
-#pragma unroll
-          for (int w = 0; w < D / 64; ++w) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (u < p.T)
-              x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + b * p.vs.b + hkv * p.vs.h +
-                                                       u * p.vs.n + r8 * (D / 8) + 8 * w));
-            vh[i][4 * w] = x.x;
-            vh[i][4 * w + 1] = x.y;
-            vh[i][4 * w + 2] = x.z;
-            vh[i][4 * w + 3] = x.w;
-            if (DT<QT>::kCoarse) vt = amax2(amax2(amax2(amax2(vt, x.x), x.y), x.z), x.w);
+          for (int n = 0; n < NR; ++n) {
+            MmaOp<MT16>::run(s[n], a0, qb[n][2 * w][0], qb[n][2 * w][1]);
+            MmaOp<MT16>::run(s[n], a1, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
           }
-          lg[i] = 0.f;
-          rv[i] = 1.f;
-          if (DT<QT>::kCoarse) {
+        }
+        // the power of value row 4 q + i; the scores' rows (slots r8, r8 + 8) take theirs from the lanes that have it
+        float vdown[4] = {1.f, 1.f, 1.f, 1.f};
+        int ve[4] = {0, 0, 0, 0};
+        if (DT<QT>::kCoarse) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t vt = 0;
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+              const uint4 x = part(vn, p.vs.n, u0 + 4 * q4 + i, r8 * (D / 8) + 8 * w);
+              vt = amax2(amax2(amax2(amax2(vt, x.x), x.y), x.z), x.w);
+            }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) vt = max(vt, __shfl_xor_sync(0xffffffffu, vt, o));
-            const int e = exp_of(vt);
-            lg[i] = (float)e;
-            rv[i] = pow2i(-e);
-#pragma unroll
-            for (int w = 0; w < D / 16; ++w) vh[i][w] = to_half2<QT>(vh[i][w], rv[i]);
+            ve[i] = exp_of(vt);
+            vdown[i] = pow2i(-ve[i]);
           }
-#pragma unroll
-          for (int w = 0; w < D / 16; ++w) vh[i][w] = clean2<__half>(vh[i][w], odd);
         }
+        float rv[2];
+        float lm[NR][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int u = u0 + 4 * q4 + i;
+        for (int n = 0; n < NR; ++n) lm[n][0] = lm[n][1] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e0 = __shfl_sync(0xffffffffu, ve[2 * j], r8 >> 1), e1 = __shfl_sync(0xffffffffu, ve[2 * j + 1], r8 >> 1);
+          const int ev = r8 & 1 ? e1 : e0;
+          rv[j] = pow2i(-ev);
+          const int u = u0 + key0 + 2 * j;
           const int du = u < p.T ? max(__popcll(node_mask(p, b, u)) - 1, 0) : 0;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float z = 0.f;
-              if (p.z && row[mt][e].z) z = row[mt][e].z[iclamp(du - row[mt][e].depth, p.e_lo, p.e_hi) - p.e_lo];
-              float& x = s[mt][i >> 1][2 * e + (i & 1)];
-              const bool keep = u < p.T && ((row[mt][e].mask >> (u & 63)) & 1ull);
-              x = keep ? fmaf(x, kcol[i], lg[i] + z) : -INFINITY;
+              const int r = row_of(n, e);
+              const unsigned long long mk = r < R ? node_mask(p, b, r / p.G) : 0ull;
+              float x = (float)ev;
+              if (p.z) x += z_of(n, e)[iclamp(du - max(__popcll(mk) - 1, 0), p.e_lo, p.e_hi) - p.e_lo];
+              const bool keep = u < p.T && ((mk >> (u & 63)) & 1ull);
+              float& y = s[n][2 * j + e];
+              y = keep ? fmaf(y, kcol[j], x) : -INFINITY;
+              lm[n][e] = fmaxf(lm[n][e], y);
             }
         }
-        new_max(s);
-        uint32_t pa[MT][4];
+        new_max(lm);
+        uint32_t pb[NR][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < NR; ++n) {
+          const float m0 = safe(mrow[n][0]), m1 = safe(mrow[n][1]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float m0 = safe(mrow[mt][e]);
-            float w[4];
+          for (int j = 0; j < 2; ++j) {
+            const float w0 = ex2(s[n][2 * j] - m0), w1 = ex2(s[n][2 * j + 1] - m1);
+            lrow[n][0] = fmaf(w0, rv[j], lrow[n][0]);
+            lrow[n][1] = fmaf(w1, rv[j], lrow[n][1]);
+            pb[n][j] = transpose8(DT<MT16>::pack(w0, w1));
+          }
+        }
+        bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              w[i] = ex2(s[mt][i >> 1][2 * e + (i & 1)] - m0);
-              lrow[mt][e] = fmaf(w[i], rv[i], lrow[mt][e]);
-            }
-            pa[mt][e] = DT<MT16>::pack(w[0], w[1]);
-            pa[mt][2 + e] = DT<MT16>::pack(w[2], w[3]);
+        for (int w = 0; w < D / 64; ++w) {
+          uint32_t vh[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 x = part(vn, p.vs.n, u0 + 4 * q4 + i, r8 * (D / 8) + 8 * w);
+            vh[i][0] = clean2<__half>(to_half2<QT>(x.x, vdown[i]), odd);
+            vh[i][1] = clean2<__half>(to_half2<QT>(x.y, vdown[i]), odd);
+            vh[i][2] = clean2<__half>(to_half2<QT>(x.z, vdown[i]), odd);
+            vh[i][3] = clean2<__half>(to_half2<QT>(x.w, vdown[i]), odd);
           }
 #pragma unroll
-        for (int w = 0; w < D / 16; ++w)
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t a[4] = {__byte_perm(vh[0][x], vh[1][x], 0x5410), __byte_perm(vh[0][x], vh[1][x], 0x7632),
+                                   __byte_perm(vh[2][x], vh[3][x], 0x5410), __byte_perm(vh[2][x], vh[3][x], 0x7632)};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t b0 = __byte_perm(vh[0][w], vh[1][w], c ? 0x7632 : 0x5410);
-            const uint32_t b1 = __byte_perm(vh[2][w], vh[3][w], c ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) MmaOp<MT16>::run(oacc[mt][2 * w + c], pa[mt], b0, b1);
+            for (int n = 0; n < NR; ++n) MmaOp<MT16>::run(oacc[n][4 * w + x], a, pb[n][0], pb[n][1]);
           }
+        }
         if (__any_sync(0xffffffffu, odd)) add_non_finite(u0, u0 + 16);
       }
     }
 
     // ---- join the key groups of the block
-    const float cm = WIDE ? p.c2 : 1.f;                 // base-2 units of the maxima
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float l = lrow[mt][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int r = (wm * MT + mt) * 16 + r8 + 8 * e;
-        if (q4 == 0) {
-          sm_m[wn][r] = mrow[mt][e] * cm;
+        float l = lrow[n][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const int r = (wm * NR + n) * 8 + 2 * q4 + e;
+        if (r8 == 0) {
+          sm_m[wn][r] = mrow[n][e] * unit;
           sm_l[wn][r] = l;
         }
       }
     __syncthreads();                                    // also: every stage has been read
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = (wm * MT + mt) * 16 + r8 + 8 * e;
+        const int r = (wm * NR + n) * 8 + 2 * q4 + e;
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WN; ++w) m = fmaxf(m, sm_m[w][r]);
-        const float f = ex2(mrow[mt][e] * cm - safe(m));
-        float* dst = merge + (wn * ROWS + r) * D;
+        const float f = ex2(mrow[n][e] * unit - safe(m));
+        float* dst = merge + (wn * ROWS + r) * MP;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < MTD; ++i)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int slot = 2 * q4 + c;
-            dst[WIDE ? n * 8 + slot : slot * NT + n] = oacc[mt][n][2 * e + c] * f;
-          }
+          for (int c = 0; c < 2; ++c) dst[WIDE ? 16 * i + 8 * c + r8 : r8 * (D / 8) + 2 * i + c] = oacc[n][i][2 * c + e] * f;
       }
     __syncthreads();
     const bool whole = tile0 == 0 && tile1 == nt;
@@ -891,7 +883,7 @@ __global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeP
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < WN; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * D + 4 * c);
+        const float4 x = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * MP + 4 * c);
         o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
       }
       if (!whole) {
@@ -913,7 +905,7 @@ template <class TL, int FMT>
 constexpr int stage_bytes() {
   constexpr bool wide = FMT == RELPOS_CACHE_F16;
   constexpr int st = TL::WN * TL::STAGES * (2 * TL::KW * TL::D * (wide ? 2 : 1) + (wide ? 0 : TL::KW * 8));
-  constexpr int mg = TL::WN * TL::ROWS * TL::D * 4;
+  constexpr int mg = TL::WN * TL::ROWS * (TL::D + 4) * 4;
   return st > mg ? st : mg;
 }
 
@@ -934,26 +926,38 @@ cudaError_t run_tiling(const TreeParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Tilings by head dimension and row count: up to 16 and 32 rows four (or two)
-// groups of warps take different keys, beyond that the warps share the keys and
-// take different rows.
-using T64_16 = Tiling<64, 1, 4, 1, 32, 3>;
-using T64_32 = Tiling<64, 1, 4, 2, 32, 3>;
-using T64_64 = Tiling<64, 2, 2, 2, 32, 3>;
-using T128_16 = Tiling<128, 1, 4, 1, 16, 3>;
-using T128_32 = Tiling<128, 2, 2, 1, 32, 3>;
-using T128_64 = Tiling<128, 4, 1, 1, 64, 3>;
+// Tilings by head dimension and row count.  Up to 32 rows (16 at d = 128, where
+// the outputs take twice the registers) four warps take different keys; beyond
+// that warps share keys and take different rows.  Stages are sized for BPS blocks
+// to an SM with some 100 KB of loads in flight.
+template <int D, bool WIDE> struct Tilings;
+template <bool WIDE> struct Tilings<64, WIDE> {
+  using R8 = Tiling<64, 1, 4, 1, WIDE ? 16 : 32, 16, 3, 4>;
+  using R16 = Tiling<64, 1, 4, 2, WIDE ? 16 : 32, 16, 3, 4>;
+  using R32 = Tiling<64, 1, 4, 4, WIDE ? 16 : 32, 16, 3, 3>;
+  using R64 = Tiling<64, 2, 2, 4, 32, 16, 3, 3>;
+};
+template <bool WIDE> struct Tilings<128, WIDE> {
+  using R8 = Tiling<128, 1, 4, 1, 16, 16, 3, WIDE ? 2 : 4>;
+  using R16 = Tiling<128, 1, 4, 2, 16, 16, 3, WIDE ? 2 : 3>;
+  using R32 = Tiling<128, 2, 2, 2, 32, 16, 3, WIDE ? 2 : 3>;
+  using R64 = Tiling<128, 4, 1, 2, 64, 16, 3, WIDE ? 2 : 3>;
+};
+
+template <typename QT, int FMT, class T>
+cudaError_t run_rows(const TreeParams& p, cudaStream_t s) {
+  switch (p.rows_per_block) {
+    case 8: return run_tiling<typename T::R8, QT, FMT>(p, s);
+    case 16: return run_tiling<typename T::R16, QT, FMT>(p, s);
+    case 32: return run_tiling<typename T::R32, QT, FMT>(p, s);
+    default: return run_tiling<typename T::R64, QT, FMT>(p, s);
+  }
+}
 
 template <typename QT, int FMT>
 cudaError_t run_format(const TreeParams& p, cudaStream_t s) {
-  if (p.c.d == 64) {
-    if (p.rows_per_block == 16) return run_tiling<T64_16, QT, FMT>(p, s);
-    if (p.rows_per_block == 32) return run_tiling<T64_32, QT, FMT>(p, s);
-    return run_tiling<T64_64, QT, FMT>(p, s);
-  }
-  if (p.rows_per_block == 16) return run_tiling<T128_16, QT, FMT>(p, s);
-  if (p.rows_per_block == 32) return run_tiling<T128_32, QT, FMT>(p, s);
-  return run_tiling<T128_64, QT, FMT>(p, s);
+  constexpr bool wide = FMT == RELPOS_CACHE_F16;
+  return p.c.d == 64 ? run_rows<QT, FMT, Tilings<64, wide>>(p, s) : run_rows<QT, FMT, Tilings<128, wide>>(p, s);
 }
 
 cudaError_t run_f16(const TreeParams& p, cudaStream_t s);
