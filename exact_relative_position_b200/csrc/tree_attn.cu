@@ -13,6 +13,7 @@ namespace {
 // row of 16 can reach (they lie before position 0) are left out.
 template <int D, typename QT>
 __global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, q4 = lane & 3, r8 = lane >> 2;
   const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 16;
   const int W = p.e_hi - p.e_lo + 1;
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ T
 
 // The bias alone: one row of offsets a head, shared by sequences and nodes.
 __global__ void __launch_bounds__(128) bias_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int e = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;
   if (e > p.e_hi - p.e_lo) return;
   const int r = iclamp(phi_of(p.map, p.N, p.e_lo + e), 0, p.R - 1);
@@ -89,6 +91,7 @@ __global__ void __launch_bounds__(128) bias_kernel(const __grid_constant__ TreeP
 // Joins the partial results of an item that was cut: pieces c0 .. c1 of the
 // line hold it, the first in the piece's last slot (unless the item begins the
 // piece), the others in their first.  Summed in the order of the pieces.
+template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p, int tk, int wide) {
   __shared__ long long sums[2][4];
   const int items = p.c.Hkv * p.row_blocks;
@@ -116,27 +119,46 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   const int nt = seq_tiles(p, b, tk, wide);
   const long long start = before * items + (long long)item * nt;
   const int c0 = (int)(start / quantum), c1 = (int)((start + nt - 1) / quantum);
+  // every block waits, the idle ones too: what follows this kernel on the stream
+  // must not start before the attention has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;                                // written whole
   const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
-  const int D = p.c.d, ROWS = p.rows_per_block;
-  const int first = start > c0 * quantum ? 1 : 0;
+  const int ROWS = p.rows_per_block;
   const long long sf = slot_floats(ROWS, D);
   const int n = min(ROWS, p.G * p.T - rb * ROWS);
-  for (int i = tid; i < n * (D / 4); i += 128) {
-    const int r = i / (D / 4), c = i - r * (D / 4);
-    float m = -INFINITY;
-    for (int k = c0; k <= c1; ++k) m = fmaxf(m, p.part[(2LL * k + (k == c0 ? first : 0)) * sf + ROWS * D + r]);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = c0; k <= c1; ++k) {
-      const float* s = p.part + (2LL * k + (k == c0 ? first : 0)) * sf;
-      const float f = ex2(s[ROWS * D + r] - safe(m));
-      const float4 x = *reinterpret_cast<const float4*>(s + (long long)r * D + 4 * c);
-      l += s[ROWS * D + ROWS + r] * f;
-      o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+  // a group of D / 4 lanes takes a row, each lane four columns; the weights of
+  // as many pieces are found at once, one to a lane
+  constexpr int GL = D / 4;
+  const int c = tid % GL, r = (blockIdx.y * 128 + tid) / GL;
+  const bool live = r < n;
+  const float* first = p.part + (2LL * c0 + (start > c0 * quantum ? 1 : 0)) * sf;
+  auto slot = [&](int k) { return k == c0 ? first : p.part + 2LL * k * sf; };
+  float m = -INFINITY;
+  for (int k = c0 + c; k <= c1; k += GL)
+    if (live) m = fmaxf(m, slot(k)[ROWS * D + r]);
+#pragma unroll
+  for (int o = 1; o < GL; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = c0; k0 <= c1; k0 += GL) {
+    float f = 0.f, lk = 0.f;
+    if (live && k0 + c <= c1) {
+      const float* s = slot(k0 + c);
+      f = ex2(s[ROWS * D + r] - safe(m));
+      lk = s[ROWS * D + ROWS + r];
     }
-    store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
+    const int nk = min(GL, c1 - k0 + 1);
+#pragma unroll 4
+    for (int i = 0; i < nk; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i, GL), li = __shfl_sync(0xffffffffu, lk, i, GL);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (live) x = *reinterpret_cast<const float4*>(slot(k0 + i) + (long long)r * D + 4 * c);
+      l = fmaf(li, fi, l);
+      o.x = fmaf(x.x, fi, o.x); o.y = fmaf(x.y, fi, o.y); o.z = fmaf(x.z, fi, o.z); o.w = fmaf(x.w, fi, o.w);
+    }
   }
+  if (live) store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
 }
 
 // Keys to a tile and blocks to an SM of the tiling a call takes.
@@ -209,9 +231,10 @@ cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_combine(const TreeParams& p, cudaStream_t s) {
-  combine_kernel<<<p.B * p.c.Hkv * p.row_blocks, 128, 0, s>>>(p, shape_of(p).tk, wide_cache(p));
+  const dim3 grid(p.B * p.c.Hkv * p.row_blocks, (p.rows_per_block * p.c.d / 4 + 127) / 128);
   note_launch(1);
-  return cudaGetLastError();
+  const int tk = shape_of(p).tk, wide = wide_cache(p);
+  return launch_after(p.c.d == 64 ? combine_kernel<64> : combine_kernel<128>, grid, 0, s, true, p, tk, wide);
 }
 
 }  // namespace relpos

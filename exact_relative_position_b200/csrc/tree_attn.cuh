@@ -269,13 +269,15 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   constexpr int SG = TL::SK / 16;                       // groups of 16 keys to a step
   constexpr int HALF = KW * CPR * 16;                   // bytes of a group's keys (or values) in a stage
   constexpr int GSTAGE = 2 * HALF + (WIDE ? 0 : KW * 8);
-  constexpr int MP = D + 4;                             // pitch of the rows that the warps join
   using MT16 = typename std::conditional<WIDE, QT, __half>::type;   // operand type of the MMAs
 
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sums[4];
   __shared__ uint32_t valid_bits[WN][TL::STAGES][(KW + 31) / 32];
   __shared__ float sm_m[WN][ROWS], sm_l[WN][ROWS];
+  __shared__ const float* row_z[ROWS];                  // relation terms of a row at offset e_lo
+  __shared__ unsigned long long row_mask[ROWS];         // nodes it attends (0: padding, or no row)
+  __shared__ int row_depth[ROWS], node_depth[64];
   int* pre = reinterpret_cast<int*>(smem);              // [B + 1], rounded up to 128 bytes
   const uint32_t pre_bytes = (uint32_t)((p.B + 1) * 4 + 127) & ~127u;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   const int q4 = lane & 3, r8 = lane >> 2;
   const int key0 = 4 * (r8 >> 1) + (r8 & 1);            // key (of 16) of row slot r8; slot r8 + 8: two more
   const uint32_t stage0 = smem_u32(smem) + pre_bytes + (uint32_t)(wn * TL::STAGES * GSTAGE);
-  float* merge = reinterpret_cast<float*>(smem + pre_bytes);   // [WN][ROWS][MP], over the stages
+  static_assert(GSTAGE >= WM * 8 * D * 4, "a stage holds eight rows of outputs of each of its warps");
 
   auto group_sync = [&]() {
     if (WM == 1) __syncwarp();
@@ -298,92 +300,148 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   line.items = p.c.Hkv * p.row_blocks;
   line.total = (long long)pre[p.B] * line.items;
   line.quantum = (line.total + gridDim.x - 1) / gridDim.x;
-  long long cur = line.quantum * blockIdx.x;
-  const long long my_start = cur;
-  const long long my_end = min(line.total, cur + line.quantum);
+  const long long my_start = line.quantum * blockIdx.x;
+  const long long my_end = min(line.total, my_start + line.quantum);
+  if (my_start >= my_end) return;
   const int page_mask = (1 << p.c.page_shift) - 1;
   const int R = p.G * p.T;
 
-  while (cur < my_end) {
-    const int b = line.seq_of(cur);
-    const int nt = pre[b + 1] - pre[b];
-    const long long in_b = cur - (long long)pre[b] * line.items;
-    const int item = (int)(in_b / nt), tile0 = (int)(in_b - (long long)item * nt);
-    const int tile1 = (int)min((long long)nt, tile0 + (my_end - cur));
-    const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
-    const int len = seq_len(p, b);
+  // Two places on the line: the tile that is loaded next and the one that is
+  // computed.  Loads run ahead across the borders of items.
+  struct Place {
+    long long at;
+    int b, item, tile, nt, len, hkv;
+  };
+  auto seat = [&](Place& c) {
+    c.b = line.seq_of(c.at);
+    c.nt = pre[c.b + 1] - pre[c.b];
+    const long long in_b = c.at - (long long)pre[c.b] * line.items;
+    c.item = (int)(in_b / c.nt);
+    c.tile = (int)(in_b - (long long)c.item * c.nt);
+    c.hkv = c.item / p.row_blocks;
+    c.len = seq_len(p, c.b);
+  };
+  auto advance = [&](Place& c, int tiles) {             // to the next tile, or the next item's first
+    c.at += tiles;
+    c.tile += tiles;
+    if (c.tile < c.nt) return;
+    c.tile = 0;
+    if (++c.item == line.items) {
+      c.item = 0;
+      if (++c.b >= p.B) return;
+      c.nt = pre[c.b + 1] - pre[c.b];
+      c.len = seq_len(p, c.b);
+    }
+    c.hkv = c.item / p.row_blocks;
+  };
 
-    // ---- loads: rows of the cache by page, nodes behind them (16-bit cache)
-    const uint8_t* kc_base = static_cast<const uint8_t*>(p.c.k);
-    const uint8_t* vc_base = static_cast<const uint8_t*>(p.c.v);
-    const int* table = p.page_table + (long long)b * p.P;
-    constexpr int LR = (KW + 31) / 32;                  // rows whose place a lane looks up
-    auto lookup = [&](int tile, uint32_t (&at)[LR]) {
-      // row of the cache of key `tile * TK + wn * KW + 32 i + lane`; all ones: none
+  // ---- loads: rows of the cache by page, nodes behind them (16-bit cache)
+  const uint8_t* kc_base = static_cast<const uint8_t*>(p.c.k);
+  const uint8_t* vc_base = static_cast<const uint8_t*>(p.c.v);
+  constexpr int LR = (KW + 31) / 32;                    // rows whose place a lane looks up
+  auto lookup = [&](const Place& c, uint32_t (&at)[LR]) {
+    // row of the cache of the group's key 32 i + lane; all ones: none
 #pragma unroll
-      for (int i = 0; i < LR; ++i) {
-        const int lr = 32 * i + lane, j = tile * TK + wn * KW + lr;
-        at[i] = 0xffffffffu;
-        if (lr < KW && tile < tile1 && j < len) {
-          const int id = __ldg(table + (j >> p.c.page_shift));
-          if (id >= 0 && id < p.c.num_pages)
-            at[i] = (((uint32_t)id * (uint32_t)p.c.Hkv + (uint32_t)hkv) << p.c.page_shift) + (uint32_t)(j & page_mask);
-        }
+    for (int i = 0; i < LR; ++i) {
+      const int lr = 32 * i + lane, j = c.tile * TK + wn * KW + lr;
+      at[i] = 0xffffffffu;
+      if (lr < KW && c.at < my_end && j < c.len) {
+        const int id = __ldg(p.page_table + (long long)c.b * p.P + (j >> p.c.page_shift));
+        if (id >= 0 && id < p.c.num_pages)
+          at[i] = (((uint32_t)id * (uint32_t)p.c.Hkv + (uint32_t)c.hkv) << p.c.page_shift) + (uint32_t)(j & page_mask);
       }
-    };
-    auto issue = [&](int tile, int stage, const uint32_t (&at)[LR]) {
-      const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
-      const int k0 = tile * TK + wn * KW;
-      const bool nodes = WIDE && k0 + KW > len;         // some rows are nodes, or past the end
+    }
+  };
+  auto issue = [&](const Place& c, int stage, const uint32_t (&at)[LR]) {
+    const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
+    const int k0 = c.tile * TK + wn * KW;
+    const bool nodes = WIDE && k0 + KW > c.len;         // some rows are nodes, or past the end
 #pragma unroll
-      for (int i = 0; i < KW * CPR / GT; ++i) {
-        const int ci = i * GT + gtid, r = ci / CPR, ch = ci % CPR;
-        const uint32_t at_r = __shfl_sync(0xffffffffu, at[(LR > 1) ? (i * GT / CPR) / 32 : 0], r & 31);
-        const uint8_t *ksrc = kc_base, *vsrc = vc_base;
-        int bytes = 0;
-        if (at_r != 0xffffffffu) {
-          const unsigned long long off = (unsigned long long)at_r * (D * ES) + ch * 16;
-          ksrc += off;
-          vsrc += off;
+    for (int i = 0; i < KW * CPR / GT; ++i) {
+      const int ci = i * GT + gtid, r = ci / CPR, ch = ci % CPR;
+      const uint32_t at_r = __shfl_sync(0xffffffffu, at[(LR > 1) ? (i * GT / CPR) / 32 : 0], r & 31);
+      const uint8_t *ksrc = kc_base, *vsrc = vc_base;
+      int bytes = 0;
+      if (at_r != 0xffffffffu) {
+        const unsigned long long off = (unsigned long long)at_r * (D * ES) + ch * 16;
+        ksrc += off;
+        vsrc += off;
+        bytes = 16;
+      } else if (nodes) {
+        const int u = k0 + r - c.len;
+        if (u >= 0 && u < p.T) {
+          ksrc = static_cast<const uint8_t*>(p.k) + 2 * (c.b * p.ks.b + c.hkv * p.ks.h + u * p.ks.n + ch * 8);
+          vsrc = static_cast<const uint8_t*>(p.v) + 2 * (c.b * p.vs.b + c.hkv * p.vs.h + u * p.vs.n + ch * 8);
           bytes = 16;
-        } else if (nodes) {
-          const int u = k0 + r - len;
-          if (u >= 0 && u < p.T) {
-            ksrc = static_cast<const uint8_t*>(p.k) + 2 * (b * p.ks.b + hkv * p.ks.h + u * p.ks.n + ch * 8);
-            vsrc = static_cast<const uint8_t*>(p.v) + 2 * (b * p.vs.b + hkv * p.vs.h + u * p.vs.n + ch * 8);
-            bytes = 16;
-          }
         }
-        cp_async16(sk + chunk_at<CPR, WIDE, false>(r, ch), ksrc, bytes);
-        cp_async16(sv + chunk_at<CPR, WIDE, true>(r, ch), vsrc, bytes);
       }
+      cp_async16(sk + chunk_at<CPR, WIDE, false>(r, ch), ksrc, bytes);
+      cp_async16(sv + chunk_at<CPR, WIDE, true>(r, ch), vsrc, bytes);
+    }
 #pragma unroll
-      for (int i = 0; i < LR; ++i) {
-        const int lr = 32 * i + lane;
-        bool ok = at[i] != 0xffffffffu;
-        if (nodes) ok = ok || (lr < KW && k0 + lr >= len && k0 + lr < len + p.T);
-        const uint32_t bits = __ballot_sync(0xffffffffu, ok);
-        if (wm == 0 && lane == 0) valid_bits[wn][stage][i] = bits;
-        if (!WIDE && wm == 0 && lr < KW) {
-          const uint32_t ss = sk + 2 * HALF + lr * 4;
-          const uint32_t src = ok ? at[i] : 0u;
-          cp_async4(ss, p.c.ks + src, ok ? 4 : 0);
-          cp_async4(ss + KW * 4, p.c.vs + src, ok ? 4 : 0);
-        }
+    for (int i = 0; i < LR; ++i) {
+      const int lr = 32 * i + lane;
+      bool ok = at[i] != 0xffffffffu;
+      if (nodes) ok = ok || (lr < KW && k0 + lr >= c.len && k0 + lr < c.len + p.T);
+      const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+      if (wm == 0 && lane == 0) valid_bits[wn][stage][i] = bits;
+      if (!WIDE && wm == 0 && lr < KW) {
+        const uint32_t ss = sk + 2 * HALF + lr * 4;
+        const uint32_t src = ok ? at[i] : 0u;
+        cp_async4(ss, p.c.ks + src, ok ? 4 : 0);
+        cp_async4(ss + KW * 4, p.c.vs + src, ok ? 4 : 0);
       }
-    };
+    }
+  };
 
-    uint32_t at_next[LR];
-    {
-      uint32_t at[TL::STAGES - 1][LR];
+  Place ld, cp;
+  ld.at = my_start;
+  seat(ld);
+  cp = ld;
+  uint32_t at_next[LR];
+  {
+    uint32_t at[TL::STAGES - 1][LR];
+    Place c = ld;
 #pragma unroll
-      for (int s = 0; s < TL::STAGES - 1; ++s) lookup(tile0 + s, at[s]);
-      lookup(tile0 + TL::STAGES - 1, at_next);
+    for (int s = 0; s < TL::STAGES - 1; ++s) {          // all look-ups first: their latencies overlap
+      lookup(c, at[s]);
+      advance(c, 1);
+    }
+    lookup(c, at_next);
 #pragma unroll
-      for (int s = 0; s < TL::STAGES - 1; ++s) {
-        if (tile0 + s < tile1) issue(tile0 + s, s, at[s]);
-        cp_async_commit();
+    for (int s = 0; s < TL::STAGES - 1; ++s) {
+      if (ld.at < my_end) issue(ld, s, at[s]);
+      cp_async_commit();
+      advance(ld, 1);
+    }
+  }
+  int stage = 0;
+  // what ran before this kernel has been waited for by the relation kernel, where
+  // there is one; its own results are read from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+#pragma unroll 1
+  while (cp.at < my_end) {
+    const int b = cp.b, nt = cp.nt, hkv = cp.hkv, len = cp.len;
+    const int rb = cp.item - hkv * p.row_blocks;
+    const int tile0 = cp.tile, tile1 = (int)min((long long)nt, tile0 + (my_end - cp.at));
+    const bool first_item = cp.at == my_start;
+
+    // ---- the rows of the item
+    if (tid < ROWS) {
+      const int r = rb * ROWS + tid;
+      unsigned long long mk = 0;
+      const float* z = p.z;
+      if (r < R) {
+        const int t = r / p.G, h = hkv * p.G + (r - t * p.G);
+        mk = node_mask(p, b, t);
+        z += b * p.z_b + h * p.z_h + t * p.z_t;
       }
+      row_mask[tid] = mk;
+      row_depth[tid] = max(__popcll(mk) - 1, 0);
+      row_z[tid] = z;
+    } else if (tid - 64 >= 0 && tid - 64 < p.T) {
+      node_depth[tid - 64] = max(__popcll(node_mask(p, b, tid - 64)) - 1, 0);
     }
 
     // ---- queries: B fragments in the permuted k order, row r8 of each tile
@@ -423,17 +481,14 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
     }
     const float kc = p.c2 * qf;                         // scores of 8-bit keys: acc * scale_j * kc (base 2)
 
-    // ---- rows 2 q and 2 q + 1 of each tile: their relation terms
-    auto row_of = [&](int n, int e) { return rb * ROWS + (wm * NR + n) * 8 + 2 * q4 + e; };
-    auto z_of = [&](int n, int e) -> const float* {     // at offset e_lo; any row's for a row that is none
-      const int r = min(row_of(n, e), R - 1), t = r / p.G, h = hkv * p.G + (r - t * p.G);
-      return p.z + b * p.z_b + h * p.z_h + t * p.z_t;
-    };
+    // ---- rows 2 q and 2 q + 1 of each tile: their saturated relation terms
+    __syncthreads();
+    auto row_of = [&](int n, int e) { return (wm * NR + n) * 8 + 2 * q4 + e; };   // in the block
     float zlow[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) zlow[n][e] = p.z ? z_of(n, e)[0] : 0.f;
+      for (int e = 0; e < 2; ++e) zlow[n][e] = p.z ? row_z[row_of(n, e)][0] : 0.f;
 
     float oacc[NR][MTD][4];
     float mrow[NR][2], lrow[NR][2];
@@ -485,8 +540,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
             for (int n = 0; n < NR; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int r = row_of(n, e);
-                if (r < R && ((node_mask(p, b, r / p.G) >> u) & 1ull)) oacc[n][i][2 * c + e] += x;
+                if ((row_mask[row_of(n, e)] >> u) & 1ull) oacc[n][i][2 * c + e] += x;
               }
           }
       }
@@ -503,24 +557,21 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         for (int g = 0; g < SG; ++g)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[n][g][i] = WIDE && EASY ? zlow[n][i & 1] : 0.f;
-      float z[NR][SG][4];
+      float z[NR][SG][4];                               // loaded before the MMAs, added after them
       if (!EASY && p.z) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float* zr = z_of(n, e);
-            const int r = min(row_of(n, e), R - 1);
-            const int depth = max(__popcll(node_mask(p, b, r / p.G)) - 1, 0);
+            const float* zr = row_z[row_of(n, e)] - p.e_lo;
+            const int depth = row_depth[row_of(n, e)];
 #pragma unroll
             for (int g = 0; g < SG; ++g)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 int at = k0 + ko + 16 * g + key0 + 2 * j - len;
-                if (WIDE && at >= 0) at = at < p.T ? max(__popcll(node_mask(p, b, at)) - 1, 0) : 0;
-                const float x = zr[iclamp(at - depth, p.e_lo, p.e_hi) - p.e_lo];
-                if (WIDE) s[n][g][2 * j + e] = x;
-                else z[n][g][2 * j + e] = x;
+                if (WIDE && at >= 0) at = at < p.T ? node_depth[at] : 0;
+                z[n][g][2 * j + e] = zr[iclamp(at - depth, p.e_lo, p.e_hi)];
               }
           }
       }
@@ -551,6 +602,14 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
             }
           }
         }
+      }
+      if (WIDE && !EASY && p.z) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int g = 0; g < SG; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][g][i] += z[n][g][i];
       }
       float rsv[SG][2];                                 // 1 / value scale of the thread's keys
       if (!WIDE) {
@@ -587,10 +646,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 bool keep = there;
-                if (WIDE && there && u >= 0) {
-                  const int r = row_of(n, e);
-                  keep = r < R && ((node_mask(p, b, r / p.G) >> u) & 1ull);
-                }
+                if (WIDE && there && u >= 0) keep = (row_mask[row_of(n, e)] >> u) & 1ull;
                 if (!keep) s[n][g][2 * j + e] = -INFINITY;
               }
           }
@@ -682,18 +738,17 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       if (WIDE && !EASY && __any_sync(0xffffffffu, odd)) add_non_finite(k0 + ko - len, k0 + ko + TL::SK - len);
     };
 
-    int stage = 0;
 #pragma unroll 1
     for (int tile = tile0; tile < tile1; ++tile) {
       cp_async_wait<TL::STAGES - 2>();
       group_sync();
       {
-        const int nx = tile + TL::STAGES - 1;
         int ns = stage + TL::STAGES - 1;
         if (ns >= TL::STAGES) ns -= TL::STAGES;
-        if (nx < tile1) issue(nx, ns, at_next);
+        if (ld.at < my_end) issue(ld, ns, at_next);
         cp_async_commit();
-        lookup(nx + 1, at_next);
+        advance(ld, 1);
+        lookup(ld, at_next);
       }
       const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
       const int k0 = tile * TK + wn * KW;
@@ -711,7 +766,6 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       }
       if (++stage == TL::STAGES) stage = 0;
     }
-    cp_async_wait<0>();
 
     // ---- 8-bit caches: the nodes' own keys, straight from their 16-bit tensors,
     // 16 nodes at a time; bf16 rows enter as fp16 times a power of two that
@@ -786,15 +840,15 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
           const int ev = r8 & 1 ? e1 : e0;
           rv[j] = pow2i(-ev);
           const int u = u0 + key0 + 2 * j;
-          const int du = u < p.T ? max(__popcll(node_mask(p, b, u)) - 1, 0) : 0;
+          const int du = u < p.T ? node_depth[u] : 0;
 #pragma unroll
           for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = row_of(n, e);
-              const unsigned long long mk = r < R ? node_mask(p, b, r / p.G) : 0ull;
+              const unsigned long long mk = row_mask[r];
               float x = (float)ev;
-              if (p.z) x += z_of(n, e)[iclamp(du - max(__popcll(mk) - 1, 0), p.e_lo, p.e_hi) - p.e_lo];
+              if (p.z) x += row_z[r][iclamp(du - row_depth[r], p.e_lo, p.e_hi) - p.e_lo];
               const bool keep = u < p.T && ((mk >> (u & 63)) & 1ull);
               float& y = s[n][2 * j + e];
               y = keep ? fmaf(y, kcol[j], x) : -INFINITY;
@@ -838,6 +892,10 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       }
     }
 
+    advance(cp, tile1 - tile0);
+    // the join may be made ready while the last results are written
+    if (cp.at >= my_end) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
     // ---- join the key groups of the block
 #pragma unroll
     for (int n = 0; n < NR; ++n)
@@ -852,65 +910,94 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
           sm_l[wn][r] = l;
         }
       }
-    __syncthreads();                                    // also: every stage has been read
+    __syncthreads();                                    // also: the last tile's stage has been read
+    // Eight rows of each warp at a time, through the stage that was read last: the
+    // loads in flight go to the others.  Rows are turned against each other by
+    // eight columns, which keeps the writes of a quad apart.
+    const int freed = stage == 0 ? TL::STAGES - 1 : stage - 1;
+    auto joined = [&](int w, int m) {                   // [8][D] of warp (m, w)
+      return reinterpret_cast<float*>(smem + pre_bytes + (w * TL::STAGES + freed) * GSTAGE) + m * 8 * D;
+    };
+    const bool whole = tile0 == 0 && tile1 == nt;
+    float* slot = p.part + ((long long)blockIdx.x * 2 + (first_item ? 0 : 1)) * slot_floats(ROWS, D);
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
+    for (int n = 0; n < NR; ++n) {
+      float* dst = joined(wn, wm);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = (wm * NR + n) * 8 + 2 * q4 + e;
+        const int r = row_of(n, e);
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WN; ++w) m = fmaxf(m, sm_m[w][r]);
         const float f = ex2(mrow[n][e] * unit - safe(m));
-        float* dst = merge + (wn * ROWS + r) * MP;
 #pragma unroll
         for (int i = 0; i < MTD; ++i)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) dst[WIDE ? 16 * i + 8 * c + r8 : r8 * (D / 8) + 2 * i + c] = oacc[n][i][2 * c + e] * f;
+          for (int c = 0; c < 2; ++c) {
+            const int d = WIDE ? 16 * i + 8 * c + r8 : r8 * (D / 8) + 2 * i + c;
+            dst[(2 * q4 + e) * D + ((d + 8 * q4) & (D - 1))] = oacc[n][i][2 * c + e] * f;
+          }
       }
-    __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == nt;
-    float* slot = p.part + ((long long)blockIdx.x * 2 + (cur == my_start ? 0 : 1)) * slot_floats(ROWS, D);
-    for (int i = tid; i < ROWS * (D / 4); i += 128) {
-      const int r = i / (D / 4), c = i % (D / 4);
-      const int gr = rb * ROWS + r;
-      if (gr >= R) break;                               // rows ascend with i
-      float m = -INFINITY, l = 0.f;
+      __syncthreads();
+      for (int i = tid; i < WM * 8 * (D / 4); i += 128) {
+        const int x = i / (D / 4), c = i % (D / 4), m8 = x >> 3;
+        const int r = (m8 * NR + n) * 8 + (x & 7), gr = rb * ROWS + r;
+        if (gr >= R) continue;
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < WN; ++w) m = fmaxf(m, sm_m[w][r]);
+        for (int w = 0; w < WN; ++w) m = fmaxf(m, sm_m[w][r]);
 #pragma unroll
-      for (int w = 0; w < WN; ++w) l += sm_l[w][r] * ex2(sm_m[w][r] - safe(m));
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < WN; ++w) l += sm_l[w][r] * ex2(sm_m[w][r] - safe(m));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < WN; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * MP + 4 * c);
-        o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
-      }
-      if (!whole) {
-        *reinterpret_cast<float4*>(slot + (long long)r * D + 4 * c) = o;
-        if (c == 0) {
-          slot[ROWS * D + r] = m;
-          slot[ROWS * D + ROWS + r] = l;
+        for (int w = 0; w < WN; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(joined(w, m8) + (x & 7) * D +
+                                                            ((4 * c + 8 * ((x & 7) >> 1)) & (D - 1)));
+          o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
         }
-      } else {
-        store_row(p, b, hkv, gr, c, o, m, l);
+        if (!whole) {
+          *reinterpret_cast<float4*>(slot + (long long)r * D + 4 * c) = o;
+          if (c == 0) {
+            slot[ROWS * D + r] = m;
+            slot[ROWS * D + ROWS + r] = l;
+          }
+        } else {
+          store_row(p, b, hkv, gr, c, o, m, l);
+        }
       }
+      __syncthreads();                                  // the stage (at the end: rows and sums, too) is free again
     }
-    __syncthreads();                                    // the stages and sums are free again
-    cur += tile1 - tile0;
   }
 }
 
 template <class TL, int FMT>
 constexpr int stage_bytes() {
   constexpr bool wide = FMT == RELPOS_CACHE_F16;
-  constexpr int st = TL::WN * TL::STAGES * (2 * TL::KW * TL::D * (wide ? 2 : 1) + (wide ? 0 : TL::KW * 8));
-  constexpr int mg = TL::WN * TL::ROWS * (TL::D + 4) * 4;
-  return st > mg ? st : mg;
+  return TL::WN * TL::STAGES * (2 * TL::KW * TL::D * (wide ? 2 : 1) + (wide ? 0 : TL::KW * 8));
+}
+
+// Launches 128-thread blocks; `early`: they may start while the kernel before
+// them on the stream, which is this library's, still runs (they wait for it
+// themselves before they use its results).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*f)(P...), dim3 grid, size_t smem, cudaStream_t s, bool early, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(128);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&c, f, args...);
 }
 
 template <class TL, typename QT, int FMT>
 cudaError_t run_tiling(const TreeParams& p, cudaStream_t s) {
+  // BPS blocks to an SM of 227 KB: the stages, 4 KB of rows, sums and reserve, and a short list of sequences
+  static_assert(TL::BPS * (stage_bytes<TL, FMT>() + 4096 + 1024) <= 227 * 1024, "the blocks of a launch do not fit at once");
   static std::atomic<unsigned long long> ready{0};      // devices whose limit has been raised
   const int smem = stage_bytes<TL, FMT>() + (((p.B + 1) * 4 + 127) & ~127);
   int dev = 0;
@@ -921,9 +1008,8 @@ cudaError_t run_tiling(const TreeParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready |= 1ull << dev;
   }
-  tree_kernel<TL, QT, FMT><<<p.grid, 128, smem, s>>>(p);
   note_launch(1);
-  return cudaGetLastError();
+  return launch_after(tree_kernel<TL, QT, FMT>, dim3(p.grid), smem, s, p.z != nullptr, p);
 }
 
 // Tilings by head dimension and row count.  Up to 32 rows (16 at d = 128, where

@@ -14,50 +14,73 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
 from ._binding import (
-    BF16, F16, F32, RelPosError, RelPosMap, _check, _stream, lib, relpos_cache_read_args, relpos_cache_write_args,
-    relpos_kv_cache, relpos_map_desc, relpos_rotary_args, relpos_rotary_tensor, relpos_tree_args, table_rows,
+    BF16, F16, F32, LIBPATH, MAP_KINDS, RelPosError, RelPosMap, _check, lib, relpos_cache_read_args, relpos_cache_write_args,
+    relpos_rotary_args, relpos_tree_args, table_rows,
 )
 
 CACHE_FORMATS = {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int8: 3}
 _DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 MAX_NODES = 64
 
+# The argument blocks of the C ABI as struct formats (native alignment).  A decoding
+# step makes these calls thousands of times a second and its kernels run for a few
+# microseconds, so the blocks are packed in one go: 1 us, where setting the fields of a
+# ctypes structure one by one takes 5.
+_STRIDES = "3q3q"
+_ROTARY = struct.Struct("@8ifiPqP" + 2 * ("PPii" + _STRIDES))
+_CACHE = "6i4P"
+_WRITE = struct.Struct("@" + _CACHE + "4iPP" + _STRIDES + "P")
+_READ = struct.Struct("@" + _CACHE + "4iPPPP")
+_TREE = struct.Struct("@" + _CACHE + "6ifiii5ii6P" + _STRIDES + "3q4P")
+assert [s.size for s in (_ROTARY, _WRITE, _READ, _TREE)] == \
+    [ctypes.sizeof(c) for c in (relpos_rotary_args, relpos_cache_write_args, relpos_cache_read_args, relpos_tree_args)]
 
-class _On:
-    """The device of a call's tensors made current for its launches."""
-
-    def __new__(cls, dev):
-        return _SAME if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
-class _Same:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_SAME = _Same()
+_CALLS = None
 
 
-def _cuda(name, t, dtype, dev=None):
-    if not t.is_cuda or (dtype is not None and t.dtype != dtype):
-        raise RelPosError(f"{name} must be a CUDA tensor" + (f" of {dtype}" if dtype is not None else ""))
-    if dev is not None and t.device != dev:
-        raise RelPosError(f"{name} must be on {dev}")
+def _calls():
+    """The entry points, taking their packed blocks."""
+    global _CALLS
+    if _CALLS is None:
+        lib()
+        dll = ctypes.CDLL(LIBPATH)
+        for name in ("relpos_rotary", "relpos_cache_write", "relpos_cache_read"):
+            getattr(dll, name).argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+        dll.relpos_tree_attn.argtypes = [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        dll.relpos_tree_workspace_size.argtypes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)]
+        _CALLS = dll
+    return _CALLS
+
+
+def _launch(name, dev, *args):
+    """One call of the C ABI on the device's current stream, with the device current."""
+    index = dev.index
+    f = getattr(_CALLS or _calls(), name)
+    if torch.cuda.current_device() == index:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status, name)
+
+
+def _cuda(name, t, dtype, dev):
+    if t.device != dev or t.dtype is not dtype:
+        raise RelPosError(f"{name} must be a CUDA tensor of {dtype} on {dev}")
 
 
 def _view(name, t, packed_ok=True):
     """(B, H, N, d) and the (b, h, n) strides of [B, H, N, d] or packed [T, H, d]."""
     if t.dim() == 4:
-        return tuple(t.shape), t.stride()[:3]
+        return t.shape, t.stride()[:3]
     if t.dim() == 3 and packed_ok:
         T, H, d = t.shape
         return (1, H, T, d), (0, t.stride(1), t.stride(0))
@@ -112,6 +135,7 @@ class RotaryMap:
         # turns per position modulo 1, in units of 2^-64 (exact products: the kernel wraps them)
         steps = [int(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % (1 << 64) for x in w]
         object.__setattr__(self, "_steps", (ctypes.c_uint64 * (r // 2))(*steps))
+        object.__setattr__(self, "_steps_ptr", ctypes.addressof(self._steps))
         m = self.magnitude
         if m is None:
             m = 0.1 * math.log(self.factor) + 1.0 if self.scaling == "yarn" and self.factor > 1 else 1.0
@@ -134,10 +158,6 @@ class RotaryMap:
         return w
 
 
-def _rotary_out(x):
-    return torch.empty_like(x)
-
-
 def relpos_rotary(q, k=None, positions=None, *, rotary: RotaryMap, inverse: bool = False, out=None):
     """Rotary embedding through the C ABI (one launch for q and k; no autograd).
 
@@ -146,59 +166,63 @@ def relpos_rotary(q, k=None, positions=None, *, rotary: RotaryMap, inverse: bool
     head count.  positions: int32 or int64 [N] or [B, N] (packed: [T]), None for
     0 .. N - 1.  out: (q_out, k_out), which may be q and k themselves.  Returns the
     turned q, or (q, k)."""
-    if q.dtype not in _DTYPES:
-        raise RelPosError(f"unsupported dtype {q.dtype}")
-    _cuda("q", q, None)
-    dev = q.device
+    dt, dev = q.dtype, q.device
+    if dt not in _DTYPES or not q.is_cuda:
+        raise RelPosError(f"q must be a float16, bfloat16 or float32 CUDA tensor, not {dt} on {dev}")
     (B, H, N, d), st = _view("q", q)
     if rotary.rotary_dim > d:
         raise RelPosError("rotary_dim exceeds the head dimension")
-    pos_ptr, pos_bytes, pos_bs = None, 8, 0
+    pos_ptr, pos_bytes, pos_bs = 0, 8, 0
     if positions is not None:
-        _cuda("positions", positions, None, dev)
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise RelPosError("positions must be int32 or int64")
+        if positions.device != dev or positions.dtype not in (torch.int32, torch.int64):
+            raise RelPosError(f"positions must be int32 or int64 on {dev}")
         if positions.shape != (N,) and (q.dim() != 4 or positions.shape != (B, N)):
             raise RelPosError("positions must be [N] or [B, N] (packed: [T])")
         if N > 1 and positions.stride(-1) != 1:
             positions = positions.contiguous()
         pos_ptr, pos_bytes = positions.data_ptr(), positions.element_size()
         pos_bs = positions.stride(0) if positions.dim() == 2 else 0
-    xs = (q,) if k is None else (q, k)
-    a = relpos_rotary_args(len(xs), B, N, d, rotary.rotary_dim, int(rotary.interleaved), _DTYPES[q.dtype],
-                           int(inverse), rotary._magnitude, pos_bytes, pos_ptr, pos_bs,
-                           ctypes.cast(rotary._steps, ctypes.c_void_p))
-    if out is not None and (not isinstance(out, (tuple, list)) or len(out) != len(xs)):
+    if out is not None and (not isinstance(out, (tuple, list)) or len(out) != (1 if k is None else 2)):
         raise RelPosError("out must hold one tensor for each input")
-    ys, keep = [], []
-    for i, x in enumerate(xs):
-        if i:
-            _cuda("k", x, q.dtype, dev)
-            (Bk, Hk, Nk, dk), st = _view("k", x)
-            if (Bk, Nk, dk) != (B, N, d) or x.dim() != q.dim():
-                raise RelPosError("k must match q in all but the head count")
-            H = Hk
-        if x.stride(-1) != 1 and d > 1:
-            if out is not None and out[i] is x:
-                raise RelPosError("the last dimension must be contiguous")
-            x = x.contiguous()
-            keep.append(x)
-            st = _view("x", x)[1]
-        y = _rotary_out(x) if out is None else out[i]
-        if out is not None:
-            _cuda("out", y, x.dtype, dev)
-            if y.shape != x.shape or (d > 1 and y.stride(-1) != 1):
-                raise RelPosError("out must have its input's shape and a contiguous last dimension")
-            if 0 in (s for s, n in zip(y.stride(), y.shape) if n > 1):
-                raise RelPosError("out must not be an expanded tensor")
-            if y.data_ptr() == x.data_ptr() and y.stride() != x.stride():
-                raise RelPosError("an output in place must have its input's strides")
-        yst = _view("out", y)[1]
-        a.t[i] = relpos_rotary_tensor(x.data_ptr(), y.data_ptr(), H, 0, *st, *yst)
-        ys.append(y)
-    with _On(dev):
-        _check(lib().relpos_rotary(ctypes.byref(a), _stream(dev)), "relpos_rotary")
-    return ys[0] if k is None else tuple(ys)
+    yq, blocks, x_q = _rotary_tensor(q, H, st, None if out is None else out[0])
+    if k is not None:
+        _cuda("k", k, dt, dev)
+        (Bk, Hk, Nk, dk), st = _view("k", k)
+        if (Bk, Nk, dk) != (B, N, d) or k.dim() != q.dim():
+            raise RelPosError("k must match q in all but the head count")
+        yk, more, x_k = _rotary_tensor(k, Hk, st, None if out is None else out[1])
+        blocks += more
+    else:
+        blocks += _NO_TENSOR
+    a = _ROTARY.pack(1 if k is None else 2, B, N, d, rotary.rotary_dim, rotary.interleaved, _DTYPES[dt], inverse,
+                     rotary._magnitude, pos_bytes, pos_ptr, pos_bs, rotary._steps_ptr, *blocks)
+    _launch("relpos_rotary", dev, a)
+    return yq if k is None else (yq, yk)
+
+
+_NO_TENSOR = (0,) * 10
+
+
+def _rotary_tensor(x, H, st, y):
+    """The output for x, the block's fields, and what must live until the call."""
+    d = x.shape[-1]
+    if d > 1 and x.stride(-1) != 1:
+        if y is x:
+            raise RelPosError("the last dimension must be contiguous")
+        x = x.contiguous()
+        st = _view("x", x)[1]
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _cuda("out", y, x.dtype, x.device)
+        if y.shape != x.shape or (d > 1 and y.stride(-1) != 1):
+            raise RelPosError("out must have its input's shape and a contiguous last dimension")
+        if 0 in (s for s, n in zip(y.stride(), y.shape) if n > 1):
+            raise RelPosError("out must not be an expanded tensor")
+        if y.data_ptr() == x.data_ptr() and y.stride() != x.stride():
+            raise RelPosError("an output in place must have its input's strides")
+    yst = st if y.stride() == x.stride() else _view("out", y)[1]
+    return y, (x.data_ptr(), y.data_ptr(), H, 0, *st, *yst), x
 
 
 class RotaryEmbedding(torch.autograd.Function):
@@ -209,14 +233,13 @@ class RotaryEmbedding(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(positions)
         ctx.cfg = (rotary, inverse)
-        y = relpos_rotary(q, k, positions, rotary=rotary, inverse=inverse)
-        return y
+        return relpos_rotary(q, k, positions, rotary=rotary, inverse=inverse)
 
     @staticmethod
     def backward(ctx, dq, dk=None):
         rotary, inverse = ctx.cfg
         positions, = ctx.saved_tensors
-        turn = lambda *g: RotaryEmbedding.apply(g[0], g[1] if len(g) > 1 else None, positions, rotary, not inverse)
+        turn = lambda x, y=None: rotary_embedding(x, y, positions, rotary=rotary, inverse=not inverse)
         if dq is not None and dk is not None:
             dq, dk = turn(dq, dk)
         elif dq is not None:
@@ -252,6 +275,8 @@ class KVCache:
         if coded != (k_scale is not None) or coded != (v_scale is not None):
             raise RelPosError("the 8-bit formats, and only they, take k_scale and v_scale")
         dev = k.device
+        if not k.is_cuda:
+            raise RelPosError("a cache lies in CUDA memory")
         for name, t, dt in (("k", k, k.dtype), ("v", v, k.dtype), ("k_scale", k_scale, torch.float32),
                             ("v_scale", v_scale, torch.float32)):
             if t is None:
@@ -264,9 +289,9 @@ class KVCache:
         self.dtype, self.device, self.coded = k.dtype, dev, coded
         if self.page_size < 1 or self.page_size & (self.page_size - 1):
             raise RelPosError("page_size must be a power of two")
-        self._c = relpos_kv_cache(self.num_pages, self.page_size, self.kv_heads, self.d, CACHE_FORMATS[k.dtype], 0,
-                                  k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if coded else None,
-                                  v_scale.data_ptr() if coded else None)
+        self._fields = (self.num_pages, self.page_size, self.kv_heads, self.d, CACHE_FORMATS[k.dtype], 0, k.data_ptr(),
+                        v.data_ptr(), k_scale.data_ptr() if coded else 0, v_scale.data_ptr() if coded else 0)
+        self._sizes = {}                                 # workspace bytes by call shape
 
 
 def kv_cache(num_pages: int, page_size: int, kv_heads: int, d: int, dtype: torch.dtype, device="cuda") -> KVCache:
@@ -289,11 +314,11 @@ def kv_cache_write(cache: KVCache, k, v, slots) -> None:
     a negative slot (or one past the pool) skips its token, and no two
     tokens of a call share one.  An 8-bit row stands for code x scale: e4m3 with the
     smallest power of two that keeps it within 448, int8 with amax / 127."""
-    dev = cache.device
-    _cuda("k", k, None, dev)
-    if k.dtype not in (torch.float16, torch.bfloat16) or (not cache.coded and k.dtype != cache.dtype):
-        raise RelPosError(f"k and v of {k.dtype} do not go into a cache of {cache.dtype}")
-    _cuda("v", v, k.dtype, dev)
+    dev, dt = cache.device, k.dtype
+    if dt not in (torch.float16, torch.bfloat16) or (not cache.coded and dt != cache.dtype):
+        raise RelPosError(f"k and v of {dt} do not go into a cache of {cache.dtype}")
+    _cuda("k", k, dt, dev)
+    _cuda("v", v, dt, dev)
     _cuda("slots", slots, torch.int64, dev)
     (B, H, N, d), ks = _view("k", k)
     if v.shape != k.shape or H != cache.kv_heads or d != cache.d:
@@ -304,10 +329,9 @@ def kv_cache_write(cache: KVCache, k, v, slots) -> None:
         raise RelPosError("the last dimension of k and v must be contiguous")
     if not slots.is_contiguous():
         slots = slots.contiguous()
-    a = relpos_cache_write_args(cache._c, B, N, _DTYPES[k.dtype], 0, k.data_ptr(), v.data_ptr(), *ks,
-                                *_view("v", v)[1], slots.data_ptr())
-    with _On(dev):
-        _check(lib().relpos_cache_write(ctypes.byref(a), _stream(dev)), "relpos_cache_write")
+    a = _WRITE.pack(*cache._fields, B, N, _DTYPES[dt], 0, k.data_ptr(), v.data_ptr(), *ks, *_view("v", v)[1],
+                    slots.data_ptr())
+    _launch("relpos_cache_write", dev, a)
 
 
 def kv_cache_read(cache: KVCache, page_table, cu_seqlens, *, total_tokens: Optional[int] = None, dtype=None,
@@ -342,16 +366,36 @@ def kv_cache_read(cache: KVCache, page_table, cu_seqlens, *, total_tokens: Optio
     if total_tokens is None:
         raise RelPosError("total_tokens is required without out")
     if out is None:
-        k, v = (torch.empty((total_tokens, cache.kv_heads, cache.d), device=dev, dtype=dtype) for _ in range(2))
-    a = relpos_cache_read_args(cache._c, page_table.shape[0], page_table.shape[1], int(total_tokens), _DTYPES[dtype],
-                               page_table.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr())
-    with _On(dev):
-        _check(lib().relpos_cache_read(ctypes.byref(a), _stream(dev)), "relpos_cache_read")
+        shape = (total_tokens, cache.kv_heads, cache.d)
+        k, v = torch.empty(shape, device=dev, dtype=dtype), torch.empty(shape, device=dev, dtype=dtype)
+    a = _READ.pack(*cache._fields, page_table.shape[0], page_table.shape[1], total_tokens, _DTYPES[dtype],
+                   page_table.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr())
+    _launch("relpos_cache_read", dev, a)
     return k, v
 
 
 # ---------------------------------------------------------------- attention over the cache
-_NO_MAP = relpos_map_desc()
+_NO_MAP = (0, 0, 0, 0, 0)
+
+
+def _rows(m, N):
+    """table_rows without its call for the maps whose rows are plain."""
+    return m.num_buckets if m.kind == "t5" else 2 * m.clip + 1 if m.kind == "truncated" else table_rows(m, N)
+
+
+def _workspace_bytes(cache, B, T, H, P, code, aq, b, per_head, desc, N):
+    key = (B, T, H, P, code, aq, b, desc, N)
+    need = cache._sizes.get(key)
+    if need is None:
+        fake = 256                                       # only a table's not being NULL is read
+        block = _TREE.pack(*cache._fields, B, T, H, 0, code, code, 1.0, N, P, per_head, *desc, 0, *(0,) * 15,
+                           fake if aq else 0, fake if b else 0, 0, 0)
+        n = ctypes.c_size_t()
+        _check(_calls().relpos_tree_workspace_size(block, ctypes.byref(n)), "relpos_tree_workspace_size")
+        if len(cache._sizes) >= 256:                     # shapes of a serving loop; the pool's life is longer
+            cache._sizes.clear()
+        need = cache._sizes[key] = n.value
+    return need
 
 
 def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None, b=None, *, tau: float,
@@ -375,11 +419,10 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     hold, and an identity map's is (R + 1) / 2).  Inference only: no autograd.
     Calls that may overlap on the GPU need workspaces of their own; by default each
     call takes its own from PyTorch's allocator."""
-    dev = cache.device
-    _cuda("q", q, None, dev)
-    dt = q.dtype
+    dev, dt = cache.device, q.dtype
     if dt not in (torch.float16, torch.bfloat16) or (not cache.coded and dt != cache.dtype):
         raise RelPosError(f"q of {dt} does not go with a cache of {cache.dtype}")
+    _cuda("q", q, dt, dev)
     (B, H, T, d), qs = _view("q", q, packed_ok=False)
     Hkv = cache.kv_heads
     if d != cache.d or d not in (64, 128) or H % Hkv:
@@ -397,7 +440,7 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     if page_table.dim() != 2 or page_table.shape[0] != B or lengths.shape != (B,) \
             or not page_table.is_contiguous() or not lengths.is_contiguous():
         raise RelPosError("page_table must be contiguous [B, P] and lengths [B]")
-    mask_ptr, per_seq = None, 0
+    mask_ptr, per_seq = 0, 0
     if tree_mask is not None:
         _cuda("tree_mask", tree_mask, torch.int64, dev)
         if tree_mask.shape not in ((T,), (B, T)) or not tree_mask.is_contiguous():
@@ -408,14 +451,14 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     if aq is not None or b is not None:
         if map is None:
             raise RelPosError("aq and b need a map")
-        desc = map.desc()
+        desc = (MAP_KINDS[map.kind], map.clip, map.num_buckets, map.max_distance, map.bidirectional)
         if max_seqlen is not None:
-            N = int(max_seqlen)
+            N = max_seqlen
         elif map.kind == "identity":
             N = ((aq.shape[-2] if aq is not None else b.shape[-1]) + 1) // 2
         else:
             N = P * cache.page_size + T
-        R = table_rows(map, N)
+        R = _rows(map, N)
         if aq is not None:
             _cuda("aq", aq, dt, dev)
             per_head = int(aq.dim() == 3)
@@ -436,37 +479,29 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     if B == 0:
         return o, lse
     code = _DTYPES[dt]
-    a = relpos_tree_args(cache._c, B, T, H, 0, code, F32 if out_f32 else code, float(tau), N, P, per_head, desc, per_seq,
-                         page_table.data_ptr(), lengths.data_ptr(), mask_ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                         *qs, *k.stride()[:3], *v.stride()[:3], None if aq is None else aq.data_ptr(),
-                         None if b is None else b.data_ptr(), o.data_ptr(), lse.data_ptr())
-    need = ctypes.c_size_t()
-    L = lib()
-    _check(L.relpos_tree_workspace_size(ctypes.byref(a), ctypes.byref(need)), "relpos_tree_workspace_size")
+    need = _workspace_bytes(cache, B, T, H, P, code, aq is not None, b is not None, per_head, desc, N)
     if workspace is None:
-        workspace = torch.empty(need.value, device=dev, dtype=torch.uint8)
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise RelPosError(f"workspace must be contiguous on {dev}")
-    with _On(dev):
-        _check(L.relpos_tree_attn(ctypes.byref(a), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                  _stream(dev)), "relpos_tree_attn")
+    a = _TREE.pack(*cache._fields, B, T, H, 0, code, F32 if out_f32 else code, tau, N, P, per_head, *desc, per_seq,
+                   page_table.data_ptr(), lengths.data_ptr(), mask_ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs,
+                   *k.stride()[:3], *v.stride()[:3], 0 if aq is None else aq.data_ptr(),
+                   0 if b is None else b.data_ptr(), o.data_ptr(), lse.data_ptr())
+    _launch("relpos_tree_attn", dev, a, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return o, lse
 
 
 def tree_workspace_size(cache: KVCache, B: int, T: int, H: int, pages_per_seq: int, aq: bool = False, b: bool = False,
                         map: Optional[RelPosMap] = None, max_seqlen: Optional[int] = None) -> int:
     """Bytes of workspace relpos_tree_attention needs for these sizes (host only)."""
-    fake = 256   # only its not being NULL is read
-    N = max_seqlen if max_seqlen is not None else pages_per_seq * cache.page_size + T
-    a = relpos_tree_args()
-    a.cache, a.B, a.T, a.H, a.pages_per_seq, a.tau, a.max_seqlen = cache._c, B, T, H, pages_per_seq, 1.0, N
-    a.dtype = a.out_dtype = BF16 if cache.dtype == torch.bfloat16 else F16
-    if map is not None:
-        a.map = map.desc()
-    a.aq, a.b = fake if aq else None, fake if b else None
-    need = ctypes.c_size_t()
-    _check(lib().relpos_tree_workspace_size(ctypes.byref(a), ctypes.byref(need)), "relpos_tree_workspace_size")
-    return need.value
+    if map is None or not (aq or b):
+        desc, N = _NO_MAP, 1
+    else:
+        desc = (MAP_KINDS[map.kind], map.clip, map.num_buckets, map.max_distance, map.bidirectional)
+        N = max_seqlen if max_seqlen is not None else pages_per_seq * cache.page_size + T
+    code = BF16 if cache.dtype == torch.bfloat16 else F16
+    return _workspace_bytes(cache, B, T, H, pages_per_seq, code, aq, b, 0, desc, N)
 
 
 def tree_masks(parents) -> torch.Tensor:
