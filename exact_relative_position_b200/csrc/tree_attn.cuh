@@ -55,7 +55,7 @@
 namespace relpos {
 namespace tree {
 
-constexpr float kMinLogScale = -100.f;   // value scales count as at least 2^-100: l stays finite
+using relpos::cp_async16;
 
 // Tiling of a row count: WM x WN warps, NR tiles of 8 query rows to a warp, KW
 // keys to a group of WM warps and stage, SK keys to a step, BPS blocks to an SM.
@@ -86,6 +86,10 @@ __device__ __forceinline__ float safe(float m) { return m == -INFINITY ? 0.f : m
 
 // ---------------------------------------------------------------- the line of tiles
 // pre[b]: tiles of one item summed over the sequences before b.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src));
+}
+
 struct Line {
   const int* pre;
   int B, items;                      // items (key head, row block) of a sequence
@@ -356,6 +360,34 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
     const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
     const int k0 = c.tile * TK + wn * KW;
     const bool nodes = WIDE && k0 + KW > c.len;         // some rows are nodes, or past the end
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < LR; ++i) all = all && (at[i] != 0xffffffffu || 32 * i + lane >= KW);
+    if (__all_sync(0xffffffffu, all)) {                 // nearly every tile: nothing to check row by row
+      const int ch = gtid % CPR;
+      const uint8_t *ksrc = kc_base + ch * 16, *vsrc = vc_base + ch * 16;
+#pragma unroll
+      for (int i = 0; i < KW * CPR / GT; ++i) {
+        const int r = i * (GT / CPR) + gtid / CPR;
+        const uint32_t at_r = __shfl_sync(0xffffffffu, at[(LR > 1) ? (i * GT / CPR) / 32 : 0], r & 31);
+        const unsigned long long off = (unsigned long long)at_r * (D * ES);
+        cp_async16(sk + chunk_at<CPR, WIDE, false>(r, ch), ksrc + off);
+        cp_async16(sv + chunk_at<CPR, WIDE, true>(r, ch), vsrc + off);
+      }
+      if (wm == 0) {
+#pragma unroll
+        for (int i = 0; i < LR; ++i) {
+          const int lr = 32 * i + lane;
+          if (lane == 0) valid_bits[wn][stage][i] = KW >= 32 ? 0xffffffffu : (1u << (KW & 31)) - 1u;
+          if (!WIDE && lr < KW) {
+            const uint32_t ss = sk + 2 * HALF + lr * 4;
+            cp_async4(ss, p.c.ks + at[i], 4);
+            cp_async4(ss + KW * 4, p.c.vs + at[i], 4);
+          }
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < KW * CPR / GT; ++i) {
       const int ci = i * GT + gtid, r = ci / CPR, ch = ci % CPR;
