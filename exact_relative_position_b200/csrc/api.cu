@@ -854,14 +854,9 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
   p->vs = strides(a->v_stride_b, a->v_stride_h, a->v_stride_n);
   p->o = a->o; p->lse = a->lse;
   p->c2 = a->tau * kLog2e;
-  const int rows = p->G * a->T;
-  p->rows_per_block = tree_rows_per_block(rows);
-  p->row_blocks = (rows + p->rows_per_block - 1) / p->rows_per_block;
-  if ((long long)a->B * a->cache.kv_heads * p->row_blocks > 0x7fffffffLL) return RELPOS_ERR_INVALID_ARG;
-  p->grid = tree_grid(*p);
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = up256(off + bytes); return o; };
-  L->part = take(sizeof(float) * 2 * (size_t)p->grid * (size_t)p->rows_per_block * (a->cache.d + 2));
+  take(sizeof(int));   // the status word
   L->z = 0;
   if (a->aq || a->b) {
     st = check_map(&a->map);
@@ -887,6 +882,16 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
     p->z_t = a->aq ? zw : 0;
     p->z_b = a->aq ? zw * a->T * a->H : 0;
     L->z = take(sizeof(float) * (size_t)(a->aq ? p->z_b * a->B : zw * a->H));
+  }
+  const int rows = p->G * a->T;
+  p->rows_per_block = tree_rows_per_block(*p);
+  p->row_blocks = (rows + p->rows_per_block - 1) / p->rows_per_block;
+  if ((long long)a->B * a->cache.kv_heads * p->row_blocks > 0x7fffffffLL) return RELPOS_ERR_INVALID_ARG;
+  p->grid = tree_grid(*p);
+  L->part = take(sizeof(float) * 2 * (size_t)p->grid * (size_t)p->rows_per_block * (a->cache.d + 2));
+  {
+    const unsigned long long lim = g_wait_limit_ns.load();
+    p->wait_ns = lim ? lim : (unsigned long long)sm100::kTimeoutNs;
   }
   L->end = off;
   return RELPOS_OK;
@@ -997,10 +1002,12 @@ RELPOS_EXPORT int relpos_tree_attn(const relpos_tree_args* a, void* workspace, s
   if (reinterpret_cast<uintptr_t>(a->tree_mask) & 7) return RELPOS_ERR_INVALID_ARG;
   if (!workspace || ws_bytes < L.end || (reinterpret_cast<uintptr_t>(workspace) & 255)) return RELPOS_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.status = reinterpret_cast<int*>(ws);
   p.part = reinterpret_cast<float*>(ws + L.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (a->aq || a->b) {
+  if (p.rows_per_block == 256) e = cudaMemsetAsync(ws, 0, sizeof(int), s);
+  if (e == cudaSuccess && (a->aq || a->b)) {
     p.z = reinterpret_cast<float*>(ws + L.z);
     e = run_phase(PH_TREE_REL, s, [&] { return launch_tree_relation(p, s); });
   }

@@ -87,12 +87,15 @@ struct TreeParams {
   const float* bias;                  // [H, R] or null
   int R, N;
   relpos_map_desc map;
+  int* status;                        // device status word (a bounded wait expired)
+  unsigned long long wait_ns;         // limit of the bounded waits
   // split work
   float* part;
   int grid, rows_per_block, row_blocks;
 };
-// Rows of query (heads times nodes) one block takes, and the blocks of a launch.
-int tree_rows_per_block(int rows);
+// Rows of query (heads times nodes) one block takes, and the blocks of a launch
+// (256: the kernel for many rows).
+int tree_rows_per_block(const TreeParams& p);
 int tree_grid(const TreeParams& p);
 cudaError_t launch_tree_relation(const TreeParams& p, cudaStream_t s);
 cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s);

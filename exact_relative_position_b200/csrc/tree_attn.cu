@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(128) bias_kernel(const __grid_constant__ TreeP
 template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p, int tk, int wide) {
   __shared__ long long sums[2][4];
+  const int ROWS = p.rows_per_block;
   const int items = p.c.Hkv * p.row_blocks;
   const int b = blockIdx.x / items, item = blockIdx.x - b * items;
   const int tid = threadIdx.x;
@@ -122,43 +123,47 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   // every block waits, the idle ones too: what follows this kernel on the stream
   // must not start before the attention has ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the narrow kernel has no waits to run out; the wide one's word was cleared before it
+  if (ROWS != 256 && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.status = 0;
   if (c0 == c1) return;                                // written whole
   const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
-  const int ROWS = p.rows_per_block;
   const long long sf = slot_floats(ROWS, D);
   const int n = min(ROWS, p.G * p.T - rb * ROWS);
   // a group of D / 4 lanes takes a row, each lane four columns; the weights of
   // as many pieces are found at once, one to a lane
   constexpr int GL = D / 4;
-  const int c = tid % GL, r = (blockIdx.y * 128 + tid) / GL;
-  const bool live = r < n;
+  const int c = tid % GL;
   const float* first = p.part + (2LL * c0 + (start > c0 * quantum ? 1 : 0)) * sf;
   auto slot = [&](int k) { return k == c0 ? first : p.part + 2LL * k * sf; };
-  float m = -INFINITY;
-  for (int k = c0 + c; k <= c1; k += GL)
-    if (live) m = fmaxf(m, slot(k)[ROWS * D + r]);
+  for (int r0 = blockIdx.y * (128 / GL); r0 < n; r0 += gridDim.y * (128 / GL)) {
+    const int r = r0 + tid / GL;
+    const bool live = r < n;
+    float m = -INFINITY;
+    for (int k = c0 + c; k <= c1; k += GL)
+      if (live) m = fmaxf(m, slot(k)[ROWS * D + r]);
 #pragma unroll
-  for (int o = 1; o < GL; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = c0; k0 <= c1; k0 += GL) {
-    float f = 0.f, lk = 0.f;
-    if (live && k0 + c <= c1) {
-      const float* s = slot(k0 + c);
-      f = ex2(s[ROWS * D + r] - safe(m));
-      lk = s[ROWS * D + ROWS + r];
-    }
-    const int nk = min(GL, c1 - k0 + 1);
+    for (int o = 1; o < GL; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = c0; k0 <= c1; k0 += GL) {
+      float f = 0.f, lk = 0.f;
+      if (live && k0 + c <= c1) {
+        const float* s = slot(k0 + c);
+        f = ex2(s[ROWS * D + r] - safe(m));
+        lk = s[ROWS * D + ROWS + r];
+      }
+      const int nk = min(GL, c1 - k0 + 1);
 #pragma unroll 4
-    for (int i = 0; i < nk; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i, GL), li = __shfl_sync(0xffffffffu, lk, i, GL);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (live) x = *reinterpret_cast<const float4*>(slot(k0 + i) + (long long)r * D + 4 * c);
-      l = fmaf(li, fi, l);
-      o.x = fmaf(x.x, fi, o.x); o.y = fmaf(x.y, fi, o.y); o.z = fmaf(x.z, fi, o.z); o.w = fmaf(x.w, fi, o.w);
+      for (int i = 0; i < nk; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i, GL), li = __shfl_sync(0xffffffffu, lk, i, GL);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) x = *reinterpret_cast<const float4*>(slot(k0 + i) + (long long)r * D + 4 * c);
+        l = fmaf(li, fi, l);
+        o.x = fmaf(x.x, fi, o.x); o.y = fmaf(x.y, fi, o.y); o.z = fmaf(x.z, fi, o.z); o.w = fmaf(x.w, fi, o.w);
+      }
     }
+    if (live) store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
   }
-  if (live) store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
 }
 
 // Keys to a tile and blocks to an SM of the tiling a call takes.
@@ -178,6 +183,7 @@ bool wide_cache(const TreeParams& p) {
   return p.c.format == RELPOS_CACHE_F16 || p.c.format == RELPOS_CACHE_BF16;
 }
 Shape shape_of(const TreeParams& p) {
+  if (p.rows_per_block == 256) return {128, 1};
   if (p.c.d == 64)
     return wide_cache(p) ? shape_rows<Tilings<64, true>>(p.rows_per_block) : shape_rows<Tilings<64, false>>(p.rows_per_block);
   return wide_cache(p) ? shape_rows<Tilings<128, true>>(p.rows_per_block) : shape_rows<Tilings<128, false>>(p.rows_per_block);
@@ -188,7 +194,11 @@ Shape shape_of(const TreeParams& p) {
 
 using namespace tree;
 
-int tree_rows_per_block(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int tree_rows_per_block(const TreeParams& p) {
+  if (wide_cache(p) && takes_wide(p)) return 256;
+  const int rows = p.G * p.T;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
 
 // One piece of the line of tiles to each block that can be resident; fewer
 // where there are fewer tiles.
@@ -222,6 +232,7 @@ cudaError_t launch_tree_relation(const TreeParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s) {
+  if (p.rows_per_block == 256) return launch_wide(p, s);
   switch (p.c.format) {
     case RELPOS_CACHE_F16: return run_f16(p, s);
     case RELPOS_CACHE_BF16: return run_bf16(p, s);
@@ -231,10 +242,10 @@ cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_combine(const TreeParams& p, cudaStream_t s) {
-  const dim3 grid(p.B * p.c.Hkv * p.row_blocks, (p.rows_per_block * p.c.d / 4 + 127) / 128);
+  const dim3 grid(p.B * p.c.Hkv * p.row_blocks, (p.rows_per_block * p.c.d / 4 + 1023) / 1024);
   note_launch(1);
   const int tk = shape_of(p).tk, wide = wide_cache(p);
-  return launch_after(p.c.d == 64 ? combine_kernel<64> : combine_kernel<128>, grid, 0, s, true, p, tk, wide);
+  return launch_after(p.c.d == 64 ? combine_kernel<64> : combine_kernel<128>, 128, grid, 0, s, true, p, tk, wide);
 }
 
 }  // namespace relpos

@@ -1008,14 +1008,14 @@ constexpr int stage_bytes() {
   return TL::WN * TL::STAGES * (2 * TL::KW * TL::D * (wide ? 2 : 1) + (wide ? 0 : TL::KW * 8));
 }
 
-// Launches 128-thread blocks; `early`: they may start while the kernel before
+// Launches `threads` to a block; `early`: they may start while the kernel before
 // them on the stream, which is this library's, still runs (they wait for it
 // themselves before they use its results).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*f)(P...), dim3 grid, size_t smem, cudaStream_t s, bool early, const A&... args) {
+template <typename F, typename... A>
+cudaError_t launch_after(F* f, int threads, dim3 grid, size_t smem, cudaStream_t s, bool early, const A&... args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = grid;
-  c.blockDim = dim3(128);
+  c.blockDim = dim3(threads);
   c.dynamicSmemBytes = smem;
   c.stream = s;
   cudaLaunchAttribute at;
@@ -1041,7 +1041,7 @@ cudaError_t run_tiling(const TreeParams& p, cudaStream_t s) {
     if (dev <= 63) ready |= 1ull << dev;
   }
   note_launch(1);
-  return launch_after(tree_kernel<TL, QT, FMT>, dim3(p.grid), smem, s, p.z != nullptr, p);
+  return launch_after(tree_kernel<TL, QT, FMT>, 128, dim3(p.grid), smem, s, p.z != nullptr, p);
 }
 
 // Tilings by head dimension and row count.  Up to 32 rows (16 at d = 128, where
@@ -1084,6 +1084,8 @@ cudaError_t run_e4m3_f16(const TreeParams& p, cudaStream_t s);
 cudaError_t run_e4m3_bf16(const TreeParams& p, cudaStream_t s);
 cudaError_t run_int8_f16(const TreeParams& p, cudaStream_t s);
 cudaError_t run_int8_bf16(const TreeParams& p, cudaStream_t s);
+bool takes_wide(const TreeParams& p);   // of a call with a 16-bit cache
+cudaError_t launch_wide(const TreeParams& p, cudaStream_t s);
 
 }  // namespace tree
 }  // namespace relpos

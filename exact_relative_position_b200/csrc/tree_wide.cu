@@ -1,0 +1,569 @@
+// tree_wide.cu -- tree attention for many rows to a key head (more than 64) over
+// a 16-bit cache, on tcgen05.
+//
+// The computation and the line of tiles are those of tree_attn.cuh; here an item
+// is 256 query rows (two tiles of 128) of one key head, so that each K/V tile
+// feeds four 128-row MMAs and the work per byte is that of a dense attention
+// layer: the tensor and exponential units bound it, not memory.
+//
+// Warp roles of a block (one to an SM, walking its piece of the line):
+//   warp 0        MMA issuer (one thread); allocates the tensor memory
+//   warps 1..3    loaders: the item's queries, then K and V tiles in turn, a warp
+//                 to a tile, into a ring of tiles.  Rows come from pages of any
+//                 size and from the nodes behind the cache, so they are gathered
+//                 with cp.async into the 128-byte-swizzled layout and handed over
+//                 with a proxy fence; rows that do not exist are filled with zeros.
+//   warps 4..7    softmax of rows 0..127 (thread r owns row r = TMEM lane r)
+//   warps 8..11   softmax of rows 128..255
+// Tensor memory: S0 columns [0, 128), S1 [128, 256), O0 [256, 256 + D), O1 [384,
+// 384 + D).  A row's 16-bit weights P replace the first half of its scores.  The
+// tensor pipe runs in issue order, PV_g(t) then QK_g(t + 1), so the scores of a
+// tile being there implies that the tile before has left O and P alone; the two
+// row tiles alternate between the tensor and the exponential units.
+#include "sm100.cuh"
+#include "tree_attn.cuh"
+
+namespace relpos {
+namespace tree {
+namespace {
+
+using namespace sm100;
+
+constexpr int kKeys = 128;              // keys of a tile
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.f;           // log2 of the largest weight before O is rescaled
+constexpr int kTileRing = 8;            // tiles whose row masks are kept
+
+template <int D> struct Wide {
+  static constexpr uint32_t kTile = 128 * D * 2;             // a K, V or Q tile
+  static constexpr int kUnits = D == 128 ? 5 : 8;            // ring of K and V tiles
+  static constexpr uint32_t kOffQ = 0, kOffKV = 2 * kTile, kOffEnd = kOffKV + kUnits * kTile;
+};
+// barriers
+constexpr int kBarQFull = 0, kBarQFree = 1, kBarSFull = 2, kBarPReady = 4, kBarOFull = 6, kBarFull = 8, kBarEmpty = 16,
+              kBarDrain = 24, kBars = 25;
+
+struct WideShared {
+  uint64_t bar[kBars];
+  uint32_t valid[kTileRing][4];
+  int odd[4];                           // item number + 1 whose nodes hold non-finite values, by its last two bits
+  int depth[2][64];
+  int abort;
+  uint32_t tmem;
+  int warp_sums[kThreads / 32];
+};
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One 16-bit row chunk as the swizzled operand layout has it: 64-column halves of
+// 128 rows x 128 bytes, chunk c of row r at (c ^ r % 8).
+__device__ __forceinline__ uint32_t wide_at(int r, int ch) {
+  return (uint32_t)((ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+template <int D, typename QT>
+__global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_constant__ TreeParams p) {
+  using W = Wide<D>;
+  constexpr int CPR = D / 8;                           // 16-byte chunks of a row
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WideShared sh;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  int* pre = reinterpret_cast<int*>(smem_raw + (sb - raw) + W::kOffEnd);
+  volatile int* abort_flag = &sh.abort;
+  auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    mbar_init(bar(kBarQFull), 3);
+    mbar_init(bar(kBarQFree), 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(kBarSFull + g), 1);
+      mbar_init(bar(kBarPReady + g), 128);
+      mbar_init(bar(kBarOFull + g), 1);
+    }
+    for (int u = 0; u < W::kUnits; ++u) {
+      mbar_init(bar(kBarFull + u), 1);
+      mbar_init(bar(kBarEmpty + u), 1);
+    }
+    mbar_init(bar(kBarDrain), 1);
+    for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+  build_line<kThreads>(p, kKeys, true, pre, sh.warp_sums);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  Line line;
+  line.pre = pre;
+  line.B = p.B;
+  line.items = p.c.Hkv * p.row_blocks;
+  line.total = (long long)pre[p.B] * line.items;
+  line.quantum = (line.total + gridDim.x - 1) / gridDim.x;
+  const long long my_start = line.quantum * blockIdx.x;
+  const long long my_end = min(line.total, my_start + line.quantum);
+  const int R = p.G * p.T;
+
+  // the piece's part of one item: tiles [t0, t1) of nt
+  struct Seg {
+    int b, hkv, rb, nt, t0, t1, len, groups;
+  };
+  auto segment = [&](long long at) {
+    Seg s;
+    s.b = line.seq_of(at);
+    s.nt = pre[s.b + 1] - pre[s.b];
+    const long long in_b = at - (long long)pre[s.b] * line.items;
+    const int item = (int)(in_b / s.nt);
+    s.t0 = (int)(in_b - (long long)item * s.nt);
+    s.t1 = (int)min((long long)s.nt, s.t0 + (my_end - at));
+    s.hkv = item / p.row_blocks;
+    s.rb = item - s.hkv * p.row_blocks;
+    s.len = seq_len(p, s.b);
+    s.groups = R - s.rb * 256 > 128 ? 2 : 1;
+    return s;
+  };
+  const uint64_t limit = p.wait_ns;
+
+  // Register split: the launch gives 168 to each of 384 threads (64512); the first
+  // warpgroup drops to 88 and the softmax warpgroups take 208: 128 x 88 + 256 x 208 = 64512.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    if (warp == 0) {
+      if (lane == 0) {
+        // ------------------------------------------------------ MMA issuer
+        constexpr bool bf = DT<QT>::kCoarse;
+        const uint32_t id_qk = idesc_f16(bf, 128, 128, false, false), id_pv = idesc_f16(bf, 128, D, false, true);
+        const uint64_t dq = sdesc_sw128(sb + W::kOffQ, 16, 1024);
+        const uint64_t dk = sdesc_sw128(sb + W::kOffKV, 16, 1024);
+        const uint64_t dv = sdesc_sw128(sb + W::kOffKV, 16384, 1024);   // 64-column halves 16 KB apart
+        constexpr uint64_t kTile16 = W::kTile >> 4;
+        auto issue_qk = [&](int g, int slot) {
+          const uint64_t a = dq + g * kTile16, k = dk + slot * kTile16;
+#pragma unroll 1
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);   // 16 KB halves, 32-byte steps
+            mma_ss(tmem + g * 128, a + off, k + off, id_qk, kk > 0);
+          }
+        };
+        auto issue_pv = [&](int g, int slot, bool acc) {
+          const uint64_t v = dv + slot * kTile16;
+#pragma unroll 1
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * kk, v + 128 * kk, id_pv, (acc || kk > 0) ? 1u : 0u);
+        };
+        uint32_t unit = 0, seg_no = 0, np[2] = {0, 0};
+        auto full = [&](uint32_t u) { return mbar_wait(bar(kBarFull + u % W::kUnits), (u / W::kUnits) & 1, abort_flag, limit); };
+        bool ok = true;
+        for (long long at = my_start; at < my_end && ok; ++seg_no) {
+          const Seg s = segment(at);
+          const int n = s.t1 - s.t0;
+          ok = mbar_wait(bar(kBarQFull), seg_no & 1, abort_flag, limit) && full(unit);
+          if (!ok) break;
+          tc_fence_after();
+          for (int g = 0; g < s.groups; ++g) {
+            issue_qk(g, unit % W::kUnits);
+            mma_commit(bar(kBarSFull + g));
+          }
+          mma_commit(bar(kBarEmpty + unit % W::kUnits));
+          if (n == 1) mma_commit(bar(kBarQFree));
+#pragma unroll 1
+          for (int t = 0; t < n && ok; ++t) {
+            const uint32_t uv = unit + 1, uk = unit + 2;
+            const bool more = t + 1 < n;
+            ok = full(uv) && (!more || full(uk));
+            for (int g = 0; g < s.groups && ok; ++g) {
+              ok = mbar_wait(bar(kBarPReady + g), np[g]++ & 1, abort_flag, limit);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(g, uv % W::kUnits, t > 0);
+              if (more) {
+                issue_qk(g, uk % W::kUnits);
+                mma_commit(bar(kBarSFull + g));
+              } else {
+                mma_commit(bar(kBarOFull + g));
+              }
+            }
+            if (!ok) break;
+            mma_commit(bar(kBarEmpty + uv % W::kUnits));
+            if (more) mma_commit(bar(kBarEmpty + uk % W::kUnits));
+            if (more && t + 2 == n) mma_commit(bar(kBarQFree));
+            unit += 2;
+          }
+          at += n;
+        }
+        // every MMA issued is done before the tensor memory is freed, whoever gave up
+        mma_commit(bar(kBarDrain));
+        mbar_drain(bar(kBarDrain), 0);
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------- loaders
+      const int lw = warp - 1;
+      uint32_t unit = 0, tile_no = 0, seg_no = 0;
+      int pending = -1;                                  // ring slot of the loads that have not been handed over
+      auto publish = [&]() {
+        if (pending < 0) return;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarFull + pending));
+        pending = -1;
+      };
+      // warp-uniform wait; what is in flight is handed over before it may block
+      auto wait = [&](int i, uint32_t parity) {
+        bool got = mbar_test(bar(i), parity);           // try_wait may sleep on what is in flight here
+        if (__all_sync(0xffffffffu, got)) return true;
+        publish();
+        got = mbar_wait(bar(i), parity, abort_flag, limit);
+        return (bool)__all_sync(0xffffffffu, got);
+      };
+      bool ok = true;
+      for (long long at = my_start; at < my_end && ok; ++seg_no) {
+        const Seg s = segment(at);
+        // ---- queries: a third of the rows to a warp
+        if (seg_no > 0) ok = wait(kBarQFree, (seg_no - 1) & 1);
+        if (!ok) break;
+        publish();
+#pragma unroll 1
+        for (int i = lw * 32 + lane; i < s.groups * 128 * CPR; i += 96) {
+          const int r = i / CPR, ch = i % CPR, gr = s.rb * 256 + r;
+          const int t = gr < R ? gr / p.G : 0, h = s.hkv * p.G + (gr < R ? gr - t * p.G : 0);
+          const uint16_t* src = static_cast<const uint16_t*>(p.q) + s.b * p.qs.b + h * p.qs.h + (long long)t * p.qs.n + ch * 8;
+          cp_async16(sb + W::kOffQ + (r >> 7) * W::kTile + wide_at(r & 127, ch), src, gr < R ? 16 : 0);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarQFull));
+        // ---- K and V tiles
+        const int* table = p.page_table + (long long)s.b * p.P;
+#pragma unroll 1
+        for (int t = s.t0; t < s.t1 && ok; ++t, ++tile_no) {
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++unit) {
+            if ((int)(unit % 3) != lw) continue;
+            const int slot = (int)(unit % W::kUnits);
+            const int k0 = t * kKeys;
+            uint32_t row[4];                             // row of the cache of key 32 i + lane; all ones: none
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = k0 + 32 * i + lane;
+              row[i] = 0xffffffffu;
+              if (j < s.len) {
+                const int id = __ldg(table + (j >> p.c.page_shift));
+                if (id >= 0 && id < p.c.num_pages)
+                  row[i] = (((uint32_t)id * (uint32_t)p.c.Hkv + (uint32_t)s.hkv) << p.c.page_shift) +
+                           (uint32_t)(j & ((1 << p.c.page_shift) - 1));
+              }
+            }
+            if (unit >= (uint32_t)W::kUnits) {
+              ok = wait(kBarEmpty + slot, (unit / W::kUnits - 1) & 1);
+              if (!ok) break;
+            }
+            if (kv == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = k0 + 32 * i + lane;
+                const uint32_t bits = __ballot_sync(0xffffffffu, row[i] != 0xffffffffu || (j >= s.len && j < s.len + p.T));
+                if (lane == 0) sh.valid[tile_no % kTileRing][i] = bits;
+              }
+              __threadfence_block();
+            }
+            publish();                                   // the tile before
+            const uint32_t dst = sb + W::kOffKV + (uint32_t)slot * W::kTile;
+            const uint8_t* base = static_cast<const uint8_t*>(kv ? p.c.v : p.c.k);
+            const Strides& st = kv ? p.vs : p.ks;
+            const uint16_t* nodes = static_cast<const uint16_t*>(kv ? p.v : p.k) + s.b * st.b + s.hkv * st.h;
+            const int ch = lane % CPR;
+            const bool all = __all_sync(0xffffffffu, row[0] != 0xffffffffu && row[1] != 0xffffffffu &&
+                                                         row[2] != 0xffffffffu && row[3] != 0xffffffffu);
+            // loops stay rolled: the block's warps run different code, and what does
+            // not fit the instruction caches costs more than the loads
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t mine = i == 0 ? row[0] : i == 1 ? row[1] : i == 2 ? row[2] : row[3];
+              if (all) {
+                const uint8_t* src = base + ch * 16;
+#pragma unroll 8
+                for (int x = 0; x < 32; x += 32 / CPR) {
+                  const int rl = x + lane / CPR;
+                  const uint32_t at_r = __shfl_sync(0xffffffffu, mine, rl);
+                  cp_async16(dst + wide_at(32 * i + rl, ch), src + (unsigned long long)at_r * (D * 2));
+                }
+                continue;
+              }
+#pragma unroll 2
+              for (int x = 0; x < 32; x += 32 / CPR) {
+                // a cached row, a node, or zeros
+                const int rl = x + lane / CPR, r = 32 * i + rl;
+                const uint32_t at_r = __shfl_sync(0xffffffffu, mine, rl);
+                const int u = k0 + r - s.len;
+                const void* src = base;
+                int bytes = 16;
+                if (at_r != 0xffffffffu) src = base + (unsigned long long)at_r * (D * 2) + ch * 16;
+                else if (u >= 0 && u < p.T) src = nodes + u * st.n + ch * 8;
+                else bytes = 0;
+                cp_async16(dst + wide_at(r, ch), src, bytes);
+              }
+            }
+            if (kv && !all && k0 + kKeys > s.len) {
+              // non-finite elements of the nodes' values are left out here and added by the rows that attend them
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              __syncwarp();
+              const int r0 = max(s.len - k0, 0), r1 = min(s.len + p.T - k0, kKeys);
+#pragma unroll 1
+              for (int r = r0 + lane / CPR; r < r1; r += 32 / CPR) {
+                const uint32_t a = dst + wide_at(r, ch);
+                const uint4 w = lds128(a);
+                bool odd = false;
+                const uint32_t c[4] = {clean2<QT>(w.x, odd), clean2<QT>(w.y, odd), clean2<QT>(w.z, odd), clean2<QT>(w.w, odd)};
+                if (odd) {
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3])
+                               : "memory");
+                  *static_cast<volatile int*>(&sh.odd[seg_no & 3]) = (int)seg_no + 1;
+                }
+              }
+            }
+            pending = slot;
+          }
+        }
+        at += s.t1 - s.t0;
+      }
+      publish();
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // ---------------------------------------------------------- softmax
+    const int g = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + t_lane + g * 128, tO = tmem + t_lane + 256 + g * 128;
+    const float c2 = p.c2;
+    uint32_t ns = 0, no = 0, tile_no = 0, seg_no = 0;
+    bool ok = true;
+    // the relation terms are read, and results written, from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (long long at = my_start; at < my_end && ok; ++seg_no) {
+      const Seg s = segment(at);
+      const int n = s.t1 - s.t0;
+      if (g >= s.groups) {
+        tile_no += n;
+        at += n;
+        continue;
+      }
+      const int gr = s.rb * 256 + g * 128 + r;
+      const bool row_ok = gr < R;
+      const int t_row = row_ok ? gr / p.G : 0, h = s.hkv * p.G + (row_ok ? gr - t_row * p.G : 0);
+      const unsigned long long mk = row_ok ? node_mask(p, s.b, t_row) : 0ull;
+      const int depth = max(__popcll(mk) - 1, 0);
+      const float* z = p.z ? p.z + s.b * p.z_b + h * p.z_h + t_row * p.z_t : nullptr;
+      const float zlow = p.z ? z[0] * c2 : 0.f;
+      // depths of the nodes, for this row tile's warps
+      named_bar_sync(1 + g, 128);
+      if (r < 64) sh.depth[g][r] = r < p.T ? max(__popcll(node_mask(p, s.b, r)) - 1, 0) : 0;
+      named_bar_sync(1 + g, 128);
+      float m_run = -INFINITY, l_run = 0.f;
+#pragma unroll 1
+      for (int t = s.t0; t < s.t1; ++t, ++tile_no) {
+        const int k0 = t * kKeys;
+        const bool got = mbar_wait(bar(kBarSFull + g), ns++ & 1, abort_flag, limit);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        tc_fence_after();
+        const volatile uint32_t* vw = sh.valid[tile_no % kTileRing];
+        const bool easy = k0 + kKeys <= s.len && (vw[0] & vw[1] & vw[2] & vw[3]) == 0xffffffffu &&
+                          (!p.z || k0 + kKeys - 1 - s.len <= p.e_lo);
+        const float rowc = easy ? zlow : 0.f;           // base-2 score: x c2 + rowc
+        if (!easy) {
+          // masks and unsaturated relation terms, 32 keys at a time, back into tensor memory
+          const float* zr = p.z ? z - p.e_lo : nullptr;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            float y[32];
+            tmem_ld32(tS + 32 * i, reinterpret_cast<uint32_t*>(y));
+            tmem_wait_ld();
+            const uint32_t bits = vw[i];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              int o = k0 + 32 * i + c - s.len;          // node, or the offset from the end of the cache
+              bool keep = (bits >> c) & 1u;
+              if (o >= 0) {
+                keep = keep && ((mk >> (o & 63)) & 1ull);
+                o = sh.depth[g][o & 63];
+              }
+              if (p.z) y[c] += zr[iclamp(o - depth, p.e_lo, p.e_hi)];
+              if (!keep) y[c] = -INFINITY;
+            }
+            tmem_st32(tS + 32 * i, reinterpret_cast<uint32_t*>(y));
+          }
+          tmem_wait_st();
+        }
+        float x[128];
+        tmem_ld32(tS, reinterpret_cast<uint32_t*>(x));
+        tmem_ld32(tS + 32, reinterpret_cast<uint32_t*>(x) + 32);
+        tmem_ld32(tS + 64, reinterpret_cast<uint32_t*>(x) + 64);
+        tmem_ld32(tS + 96, reinterpret_cast<uint32_t*>(x) + 96);
+        tmem_wait_ld();
+        float pm[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) pm[u] = fmaxf(x[u], x[u + 8]);
+#pragma unroll
+        for (int c = 16; c < 128; c += 8)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) pm[u] = fmaxf(pm[u], x[c + u]);
+        const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+        const float m_new = fmaxf(m_run, mx * c2 + rowc);
+        const bool grow = m_new > m_run + kSlack;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float alpha = grow ? ex2(m_run - m_new) : 1.f;
+          if (t > s.t0) {                               // the tile before has left O: its P V came before these scores
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t ov[32];
+              tmem_ld32(tO + c, ov);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+              tmem_st32(tO + c, ov);
+            }
+          }
+          if (grow) {
+            l_run *= alpha;
+            m_run = m_new;
+          }
+        }
+        const float sub = m_run == -INFINITY ? 0.f : rowc - m_run;
+        const float2 cc = make_float2(c2, c2), ss = make_float2(sub, sub);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int w = 0; w < 32; ++w) {
+            const float2 y = ffma2(make_float2(x[64 * q + 2 * w], x[64 * q + 2 * w + 1]), cc, ss);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum[w & 1] = fadd2(sum[w & 1], e);
+            pk[w] = DT<QT>::pack(e.x, e.y);
+          }
+          tmem_st32(tS + 32 * q, pk);
+        }
+        l_run += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kBarPReady + g));
+      }
+      if (!ok) break;
+      at += n;
+      if (at >= my_end) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      // ---- the item's (or its part's) result
+      const bool got = mbar_wait(bar(kBarOFull + g), no++ & 1, abort_flag, limit);
+      if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+      tc_fence_after();
+      const bool whole = s.t0 == 0 && s.t1 == s.nt;
+      const bool odd = s.t1 == s.nt && *static_cast<volatile int*>(&sh.odd[seg_no & 3]) == (int)seg_no + 1;
+      // a padding node, or a row with no key, gives 0; a part is joined (and divided) later
+      const bool empty = mk == 0 || l_run == 0.f;
+      const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l_run;
+      const long long out_row = ((long long)s.b * p.H + h) * p.T + t_row;
+      float* slot = p.part + ((long long)blockIdx.x * 2 + (at - n == my_start ? 0 : 1)) * slot_floats(256, D);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+        tmem_wait_ld();
+        if (odd && row_ok) {
+          for (int u = 0; u < p.T; ++u) {
+            if (!((mk >> u) & 1ull)) continue;
+            const QT* src = static_cast<const QT*>(p.v) + s.b * p.vs.b + s.hkv * p.vs.h + u * p.vs.n + c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float y = DT<QT>::to_f(src[i]);
+              if (!(fabsf(y) <= 3.4028235e38f)) o[i] += y;
+            }
+          }
+        }
+        if (row_ok) {
+          float* dst = whole ? static_cast<float*>(p.o) + out_row * D + c : slot + (long long)(g * 128 + r) * D + c;
+          if (whole && !p.o_f32) {
+            uint16_t* d16 = static_cast<uint16_t*>(p.o) + out_row * D + c;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(d16 + i) =
+                  make_uint4(DT<QT>::pack(o[i] * inv, o[i + 1] * inv), DT<QT>::pack(o[i + 2] * inv, o[i + 3] * inv),
+                             DT<QT>::pack(o[i + 4] * inv, o[i + 5] * inv), DT<QT>::pack(o[i + 6] * inv, o[i + 7] * inv));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(dst + i) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+          }
+        }
+        __syncwarp();                                   // the next load is the whole warp's
+      }
+      if (whole && row_ok) p.lse[out_row] = empty ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+      if (!whole && row_ok) {
+        slot[256 * D + g * 128 + r] = m_run;
+        slot[256 * D + 256 + g * 128 + r] = l_run;
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && *abort_flag) *p.status = kStatusTimeout;
+}
+
+template <int D, typename QT>
+cudaError_t run_wide(const TreeParams& p, cudaStream_t s) {
+  static std::atomic<unsigned long long> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int most = 227 * 1024 - (int)sizeof(WideShared) - 64;
+  const int smem = (int)Wide<D>::kOffEnd + 1024 + (((p.B + 1) * 4 + 127) & ~127);
+  if (dev > 63 || !(ready.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(tree_wide_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) ready |= 1ull << dev;
+  }
+  note_launch(1);
+  return launch_after(tree_wide_kernel<D, QT>, kThreads, dim3(p.grid), smem, s, p.z != nullptr, p);
+}
+
+}  // namespace
+
+// Whether the wide kernel takes a call: more rows than the narrow one's largest
+// block, a cache of the queries' type, and relation terms that saturate within
+// 1024 offsets (each score of an unsaturated tile is looked up by its row's thread,
+// which the narrow kernel does with fewer cache lines to an instruction); the list of
+// sequences has to fit behind the ring of tiles.
+bool takes_wide(const TreeParams& p) {
+  return p.G * p.T > 64 && p.B <= 256 && (!(p.aq || p.bias) || p.e_hi - p.e_lo <= 1024);
+}
+
+cudaError_t launch_wide(const TreeParams& p, cudaStream_t s) {
+  if (p.c.d == 64) return p.bf16 ? run_wide<64, __nv_bfloat16>(p, s) : run_wide<64, __half>(p, s);
+  return p.bf16 ? run_wide<128, __nv_bfloat16>(p, s) : run_wide<128, __half>(p, s);
+}
+
+}  // namespace tree
+}  // namespace relpos

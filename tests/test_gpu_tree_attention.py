@@ -62,6 +62,10 @@ SHAPES = [
     dict(B=1, H=4, Hkv=1, T=64, d=64, lens=[95], page=16, tree="tree"),        # 256 rows
     dict(B=2, H=6, Hkv=2, T=33, d=128, lens=[70, 3], page=16, tree="bits"),    # 99 rows
     dict(B=1, H=1, Hkv=1, T=64, d=128, lens=[0], page=16, tree="bits"),
+    dict(B=2, H=2, Hkv=1, T=33, d=64, lens=[500, 128], page=16, tree="tree"),  # 66 rows: one tile of 128
+    dict(B=2, H=8, Hkv=2, T=61, d=128, lens=[700, 64], page=8, tree="tree"),   # 244 rows: two tiles
+    dict(B=2, H=10, Hkv=2, T=64, d=64, lens=[1, 385], page=1, tree="bits"),    # 320 rows: a block of two, one of one
+    dict(B=1, H=9, Hkv=1, T=60, d=128, lens=[0], page=64, tree="padded"),      # 540 rows, no cache
 ]
 
 
@@ -105,7 +109,7 @@ def test_positions_past_the_table_are_clamped():
 
 
 @pytest.mark.parametrize("fmt", [F16, E4M3], ids=["f16", "e4m3"])
-@pytest.mark.parametrize("T,H,Hkv,d", [(1, 4, 4, 64), (4, 8, 2, 128), (20, 8, 2, 64)])
+@pytest.mark.parametrize("T,H,Hkv,d", [(1, 4, 4, 64), (4, 8, 2, 128), (20, 8, 2, 64), (48, 8, 2, 128)])
 def test_long_split_over_many_blocks(fmt, T, H, Hkv, d):
     s = make(B=3, H=H, Hkv=Hkv, T=T, d=d, lens=[9000, 1, 4097], page=64, fmt=fmt, tree="tree",
              map=rp.RelPosMap("truncated", clip=64), aq="shared", b=True)
@@ -113,6 +117,37 @@ def test_long_split_over_many_blocks(fmt, T, H, Hkv, d):
     check_tree(got, want(s), F16)
     again = call(s)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_many_rows_many_items():
+    # pieces of the line that hold several items and parts of others, one and two row tiles in turn
+    g = torch.Generator().manual_seed(7)
+    s = make(B=40, H=20, Hkv=4, T=64, d=64, lens=torch.randint(0, 700, (40,), generator=g).tolist(), tree="tree",
+             map=rp.RelPosMap("log", num_buckets=16, max_distance=64), aq="head", b=True)
+    got = call(s)
+    check_tree(got, want(s), F16)
+    for _ in range(3):
+        again = call(s)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_bounded_waits_report():
+    # a limit of one nanosecond lets the many-row kernel's waits run out: it stops, and the workspace says so
+    s = make(B=4, H=16, Hkv=2, T=32, d=128, lens=[900, 700, 1000, 50], page=16)
+    need = rp.tree_workspace_size(s["cache"], 4, 32, 16, s["table"].shape[1])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    call(s, workspace=ws)
+    assert rp.check_workspace(ws) == 0
+    rp.set_wait_limit_ns(1)
+    try:
+        call(s, workspace=ws)
+        with pytest.raises(rp.RelPosError, match="timed out"):
+            rp.check_workspace(ws)
+    finally:
+        rp.set_wait_limit_ns(0)
+    got = call(s, workspace=ws)
+    assert rp.check_workspace(ws) == 0
+    check_tree(got, want(s), F16)
 
 
 def test_many_sequences():
@@ -149,8 +184,9 @@ def test_bf16_range(fmt):
 
 @pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
 @pytest.mark.parametrize("val", [float("nan"), float("inf")])
-def test_non_finite_in_masked_places(dt, fmt, val):
-    s = make(B=2, H=2, Hkv=1, T=9, d=64, lens=[21, 130], dt=dt, fmt=fmt)
+@pytest.mark.parametrize("H", [2, 16])                  # 18 rows, 144 rows
+def test_non_finite_in_masked_places(dt, fmt, val, H):
+    s = make(B=2, H=H, Hkv=1, T=9, d=64, lens=[21, 130], dt=dt, fmt=fmt)
     # node 8 is padding; node 3 is a leaf that nobody else attends; the cache's unused rows are poisoned too
     s["mask"] = rp.tree_masks([-1, 0, 1, 1, 2, 4, 5, 6, None]).cuda()
     clean = call(s)
