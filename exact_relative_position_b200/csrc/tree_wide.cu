@@ -9,10 +9,11 @@
 // Warp roles of a block (one to an SM, walking its piece of the line):
 //   warp 0        MMA issuer (one thread); allocates the tensor memory
 //   warps 1..3    loaders: the item's queries, then K and V tiles in turn, a warp
-//                 to a tile, into a ring of tiles.  Rows come from pages of any
-//                 size and from the nodes behind the cache, so they are gathered
-//                 with cp.async into the 128-byte-swizzled layout and handed over
-//                 with a proxy fence; rows that do not exist are filled with zeros.
+//                 to a tile, into a ring of tiles.  A tile whose pages all exist
+//                 comes by TMA, a box to a page (of at least 8 rows); one with
+//                 smaller or missing pages, or with the nodes behind the cache, is
+//                 gathered with cp.async into the same 128-byte-swizzled layout
+//                 and handed over with a proxy fence, rows that do not exist as zeros.
 //   warps 4..7    softmax of rows 0..127 (thread r owns row r = TMEM lane r)
 //   warps 8..11   softmax of rows 128..255
 // Tensor memory: S0 columns [0, 128), S1 [128, 256), O0 [256, 256 + D), O1 [384,
@@ -20,10 +21,15 @@
 // tensor pipe runs in issue order, PV_g(t) then QK_g(t + 1), so the scores of a
 // tile being there implies that the tile before has left O and P alone; the two
 // row tiles alternate between the tensor and the exponential units.
+#include <cudaTypedefs.h>
+
 #include "sm100.cuh"
 #include "tree_attn.cuh"
 
 namespace relpos {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // attn_fwd.cu
+
 namespace tree {
 namespace {
 
@@ -53,6 +59,12 @@ struct WideShared {
   int warp_sums[kThreads / 32];
 };
 
+__device__ __forceinline__ void tma_rows_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(col), "r"(row)
+      : "memory");
+}
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -72,7 +84,9 @@ __device__ __forceinline__ uint32_t wide_at(int r, int ch) {
 }
 
 template <int D, typename QT>
-__global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_constant__ TreeParams p,
+                                                                const __grid_constant__ CUtensorMap tm_k,
+                                                                const __grid_constant__ CUtensorMap tm_v, int box) {
   using W = Wide<D>;
   constexpr int CPR = D / 8;                           // 16-byte chunks of a row
   extern __shared__ uint8_t smem_raw[];
@@ -156,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         constexpr uint64_t kTile16 = W::kTile >> 4;
         auto issue_qk = [&](int g, int slot) {
           const uint64_t a = dq + g * kTile16, k = dk + slot * kTile16;
-#pragma unroll 1
+#pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);   // 16 KB halves, 32-byte steps
             mma_ss(tmem + g * 128, a + off, k + off, id_qk, kk > 0);
@@ -164,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         };
         auto issue_pv = [&](int g, int slot, bool acc) {
           const uint64_t v = dv + slot * kTile16;
-#pragma unroll 1
+#pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * kk, v + 128 * kk, id_pv, (acc || kk > 0) ? 1u : 0u);
         };
@@ -217,6 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
       // -------------------------------------------------------- loaders
       const int lw = warp - 1;
       uint32_t unit = 0, tile_no = 0, seg_no = 0;
+      const int nb = box ? kKeys / box : 0;              // boxes of a tile (0: pages too small)
+      int last = -1;                                     // this warp's last tile by TMA
       int pending = -1;                                  // ring slot of the loads that have not been handed over
       auto publish = [&]() {
         if (pending < 0) return;
@@ -261,6 +277,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
             if ((int)(unit % 3) != lw) continue;
             const int slot = (int)(unit % W::kUnits);
             const int k0 = t * kKeys;
+            const uint32_t dst = sb + W::kOffKV + (uint32_t)slot * W::kTile;
+            if (nb && k0 + kKeys <= s.len) {
+              // lane i has box i, if its page exists
+              int id = 0;
+              if (lane < nb) id = __ldg(table + ((k0 + lane * box) >> p.c.page_shift));
+              if (__all_sync(0xffffffffu, id >= 0 && id < p.c.num_pages)) {
+                if (unit >= (uint32_t)W::kUnits) {
+                  ok = wait(kBarEmpty + slot, (unit / W::kUnits - 1) & 1);
+                  if (!ok) break;
+                }
+                publish();
+                if (lane == 0) {
+                  if (kv == 0)
+                    for (int i = 0; i < 4; ++i) sh.valid[tile_no % kTileRing][i] = 0xffffffffu;
+                  mbar_expect_tx(bar(kBarFull + slot), W::kTile);
+                }
+                __syncwarp();
+                if (lane < nb) {
+                  const int at = ((id * p.c.Hkv + s.hkv) << p.c.page_shift) +
+                                 ((k0 + lane * box) & ((1 << p.c.page_shift) - 1));
+                  const CUtensorMap* map = kv ? &tm_v : &tm_k;
+#pragma unroll
+                  for (int h = 0; h < D / 64; ++h)
+                    tma_rows_load(dst + h * 16384 + lane * box * 128, map, bar(kBarFull + slot), h * 64, at);
+                }
+                last = (int)unit;
+                continue;
+              }
+            }
             uint32_t row[4];                             // row of the cache of key 32 i + lane; all ones: none
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -287,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
               __threadfence_block();
             }
             publish();                                   // the tile before
-            const uint32_t dst = sb + W::kOffKV + (uint32_t)slot * W::kTile;
             const uint8_t* base = static_cast<const uint8_t*>(kv ? p.c.v : p.c.k);
             const Strides& st = kv ? p.vs : p.ks;
             const uint16_t* nodes = static_cast<const uint16_t*>(kv ? p.v : p.k) + s.b * st.b + s.hkv * st.h;
@@ -348,6 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
       }
       publish();
       asm volatile("cp.async.wait_all;" ::: "memory");
+      // after an abort nobody may have waited for the last tile; the tiles before
+      // it in this warp's turn had been consumed or are waited for by theirs
+      if (!ok && last >= 0) {
+        mbar_drain(bar(kBarFull + last % W::kUnits), (last / W::kUnits) & 1);
+        if (last >= 3) mbar_drain(bar(kBarFull + (last - 3) % W::kUnits), ((last - 3) / W::kUnits) & 1);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
@@ -545,8 +595,24 @@ cudaError_t run_wide(const TreeParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready |= 1ull << dev;
   }
+  // the cache's rows of a page as TMA boxes, where a page holds whole swizzle groups
+  // of 8 rows and rows can be counted in an int
+  const long long rows = ((long long)p.c.num_pages * p.c.Hkv) << p.c.page_shift;
+  int box = p.c.page_shift >= 3 && rows < (1LL << 31) ? 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7) : 0;
+  CUtensorMap maps[2] = {};
+  if (box) {
+    auto fn = encode_fn();
+    for (int i = 0; i < 2; ++i) {
+      const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, pitch[1] = {D * 2};
+      const cuuint32_t bx[2] = {64, (cuuint32_t)box}, one[2] = {1, 1};
+      if (!fn || fn(&maps[i], DT<QT>::kCoarse ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                    i ? p.c.v : p.c.k, dims, pitch, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        box = 0;
+    }
+  }
   note_launch(1);
-  return launch_after(tree_wide_kernel<D, QT>, kThreads, dim3(p.grid), smem, s, p.z != nullptr, p);
+  return launch_after(tree_wide_kernel<D, QT>, kThreads, dim3(p.grid), smem, s, p.z != nullptr, p, maps[0], maps[1], box);
 }
 
 }  // namespace
