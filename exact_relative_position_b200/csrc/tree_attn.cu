@@ -91,78 +91,92 @@ __global__ void __launch_bounds__(128) bias_kernel(const __grid_constant__ TreeP
 // Joins the partial results of an item that was cut: pieces c0 .. c1 of the
 // line hold it, the first in the piece's last slot (unless the item begins the
 // piece), the others in their first.  Summed in the order of the pieces.
+// Block x looks at the border between pieces x and x + 1: it joins the item cut
+// there, if that is the item's first cut.  A group of D / 4 lanes takes a row, each
+// lane four columns; the weights of as many pieces are found at once, one to a lane.
 template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p, int tk, int wide) {
-  __shared__ long long sums[2][4];
-  const int ROWS = p.rows_per_block;
-  const int items = p.c.Hkv * p.row_blocks;
-  const int b = blockIdx.x / items, item = blockIdx.x - b * items;
-  const int tid = threadIdx.x;
-  long long before = 0, all = 0;
-  for (int i = tid; i < p.B; i += 128) {
-    const int n = seq_tiles(p, i, tk, wide);
-    all += n;
-    if (i < b) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-  }
-  if ((tid & 31) == 0) {
-    sums[0][tid >> 5] = before;
-    sums[1][tid >> 5] = all;
-  }
-  __syncthreads();
-  before = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
-  all = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
-  const long long total = all * items, quantum = (total + p.grid - 1) / p.grid;
-  const int nt = seq_tiles(p, b, tk, wide);
-  const long long start = before * items + (long long)item * nt;
-  const int c0 = (int)(start / quantum), c1 = (int)((start + nt - 1) / quantum);
+  constexpr int GL = D / 4, RPB = 128 / GL;
+  extern __shared__ int pre[];
+  __shared__ int warp_sums[4];
+  const int ROWS = p.rows_per_block, tid = threadIdx.x, c = tid % GL;
+  build_line<128>(p, tk, wide != 0, pre, warp_sums);
+  Line line;
+  line.pre = pre;
+  line.B = p.B;
+  line.items = p.c.Hkv * p.row_blocks;
+  line.total = (long long)pre[p.B] * line.items;
+  line.quantum = (line.total + p.grid - 1) / p.grid;
+  const long long at = line.quantum * (blockIdx.x + 1);
+  const int b = line.seq_of(min(at, line.total - 1));
+  const int nt = pre[b + 1] - pre[b];
+  const long long in_b = at - (long long)pre[b] * line.items;
+  const int item = (int)(in_b / nt), tile = (int)(in_b - (long long)item * nt);
+  const long long start = at - tile, before = line.quantum * blockIdx.x;
+  const bool mine = at < line.total && tile > 0 && start >= before;
+  const int c0 = blockIdx.x, c1 = (int)((start + nt - 1) / line.quantum);
+  const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
+  const int n = min(ROWS, p.G * p.T - rb * ROWS);
   // every block waits, the idle ones too: what follows this kernel on the stream
   // must not start before the attention has ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the narrow kernel has no waits to run out; the wide one's word was cleared before it
   if (ROWS != 256 && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.status = 0;
-  if (c0 == c1) return;                                // written whole
-  const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
+  if (!mine) return;
   const long long sf = slot_floats(ROWS, D);
-  const int n = min(ROWS, p.G * p.T - rb * ROWS);
-  // a group of D / 4 lanes takes a row, each lane four columns; the weights of
-  // as many pieces are found at once, one to a lane
-  constexpr int GL = D / 4;
-  const int c = tid % GL;
-  const float* first = p.part + (2LL * c0 + (start > c0 * quantum ? 1 : 0)) * sf;
+  const float* first = p.part + (2LL * c0 + (start > before ? 1 : 0)) * sf;
   auto slot = [&](int k) { return k == c0 ? first : p.part + 2LL * k * sf; };
-  for (int r0 = blockIdx.y * (128 / GL); r0 < n; r0 += gridDim.y * (128 / GL)) {
-    const int r = r0 + tid / GL;
-    const bool live = r < n;
-    float m = -INFINITY;
-    for (int k = c0 + c; k <= c1; k += GL)
-      if (live) m = fmaxf(m, slot(k)[ROWS * D + r]);
+  for (int r0 = blockIdx.y * RPB; r0 < n; r0 += gridDim.y * RPB) {
+    const int r = min(r0 + tid / GL, n - 1);             // lanes past the end repeat the last row
+    // all loads of an item in up to four pieces are under way before the first is used
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c0 + i <= c1) x[i] = *reinterpret_cast<const float4*>(slot(c0 + i) + (long long)r * D + 4 * c);
+    float mk = -INFINITY, lk = 0.f;
+    if (c0 + c <= c1) {
+      mk = slot(c0 + c)[ROWS * D + r];
+      lk = slot(c0 + c)[ROWS * D + ROWS + r];
+    }
+    float m = mk;
+    for (int k = c0 + c + GL; k <= c1; k += GL) m = fmaxf(m, slot(k)[ROWS * D + r]);
 #pragma unroll
     for (int o = 1; o < GL; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float f, const float4& y) {
+      o.x = fmaf(y.x, f, o.x); o.y = fmaf(y.y, f, o.y); o.z = fmaf(y.z, f, o.z); o.w = fmaf(y.w, f, o.w);
+    };
     for (int k0 = c0; k0 <= c1; k0 += GL) {
-      float f = 0.f, lk = 0.f;
-      if (live && k0 + c <= c1) {
-        const float* s = slot(k0 + c);
-        f = ex2(s[ROWS * D + r] - safe(m));
-        lk = s[ROWS * D + ROWS + r];
+      if (k0 > c0) {
+        mk = -INFINITY;
+        lk = 0.f;
+        if (k0 + c <= c1) {
+          mk = slot(k0 + c)[ROWS * D + r];
+          lk = slot(k0 + c)[ROWS * D + ROWS + r];
+        }
       }
+      const float f = ex2(mk - safe(m));
+      float lf = lk * f;
+#pragma unroll
+      for (int q = 1; q < GL; q <<= 1) lf += __shfl_xor_sync(0xffffffffu, lf, q);
+      l += lf;
       const int nk = min(GL, c1 - k0 + 1);
+      int i = 0;
+      if (k0 == c0) {
+#pragma unroll
+        for (; i < 4; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, f, i, GL);
+          if (c0 + i <= c1) add(fi, x[i]);
+        }
+      }
 #pragma unroll 4
-      for (int i = 0; i < nk; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i, GL), li = __shfl_sync(0xffffffffu, lk, i, GL);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) x = *reinterpret_cast<const float4*>(slot(k0 + i) + (long long)r * D + 4 * c);
-        l = fmaf(li, fi, l);
-        o.x = fmaf(x.x, fi, o.x); o.y = fmaf(x.y, fi, o.y); o.z = fmaf(x.z, fi, o.z); o.w = fmaf(x.w, fi, o.w);
+      for (; i < nk; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i, GL);
+        add(fi, *reinterpret_cast<const float4*>(slot(k0 + i) + (long long)r * D + 4 * c));
       }
     }
-    if (live) store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
+    if (r0 + tid / GL < n) store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
   }
 }
 
@@ -242,10 +256,13 @@ cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_combine(const TreeParams& p, cudaStream_t s) {
-  const dim3 grid(p.B * p.c.Hkv * p.row_blocks, (p.rows_per_block * p.c.d / 4 + 1023) / 1024);
+  // a block to each border of pieces and (for the wide kernel's 256 rows, every
+  // second) group of rows
+  const int groups = p.rows_per_block * p.c.d / 512;
+  const dim3 grid(p.grid > 1 ? p.grid - 1 : 1, groups > 32 ? groups / 2 : groups);
   note_launch(1);
   const int tk = shape_of(p).tk, wide = wide_cache(p);
-  return launch_after(p.c.d == 64 ? combine_kernel<64> : combine_kernel<128>, 128, grid, 0, s, true, p, tk, wide);
+  return launch_after(p.c.d == 64 ? combine_kernel<64> : combine_kernel<128>, 128, grid, (p.B + 1) * sizeof(int), s, true, p, tk, wide);
 }
 
 }  // namespace relpos

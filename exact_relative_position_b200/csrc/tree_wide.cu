@@ -253,21 +253,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
       bool ok = true;
       for (long long at = my_start; at < my_end && ok; ++seg_no) {
         const Seg s = segment(at);
-        // ---- queries: a third of the rows to a warp
-        if (seg_no > 0) ok = wait(kBarQFree, (seg_no - 1) & 1);
-        if (!ok) break;
-        publish();
+        // ---- queries, 32 rows to a warp in turn, once the first tiles are under way
+        auto load_q = [&]() {
+          if (seg_no > 0) ok = wait(kBarQFree, (seg_no - 1) & 1);
+          if (!ok) return;
+          publish();
+          const uint16_t* q = static_cast<const uint16_t*>(p.q) + s.b * p.qs.b;
 #pragma unroll 1
-        for (int i = lw * 32 + lane; i < s.groups * 128 * CPR; i += 96) {
-          const int r = i / CPR, ch = i % CPR, gr = s.rb * 256 + r;
-          const int t = gr < R ? gr / p.G : 0, h = s.hkv * p.G + (gr < R ? gr - t * p.G : 0);
-          const uint16_t* src = static_cast<const uint16_t*>(p.q) + s.b * p.qs.b + h * p.qs.h + (long long)t * p.qs.n + ch * 8;
-          cp_async16(sb + W::kOffQ + (r >> 7) * W::kTile + wide_at(r & 127, ch), src, gr < R ? 16 : 0);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarQFull));
+          for (int i = lw; i < s.groups * 4; i += 3) {
+            const int gr = s.rb * 256 + i * 32 + lane, t = gr < R ? gr / p.G : 0;
+            const int h = s.hkv * p.G + (gr < R ? gr - t * p.G : 0), ch = lane % CPR;
+            const long long off = gr < R ? h * p.qs.h + (long long)t * p.qs.n : -1;
+#pragma unroll 4
+            for (int x = 0; x < 32; x += 32 / CPR) {
+              const int rl = x + lane / CPR, r = i * 32 + rl;
+              const long long at_r = __shfl_sync(0xffffffffu, off, rl);
+              cp_async16(sb + W::kOffQ + (r >> 7) * W::kTile + wide_at(r & 127, ch), q + (at_r < 0 ? 0 : at_r) + ch * 8,
+                         at_r < 0 ? 0 : 16);
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarQFull));
+        };
         // ---- K and V tiles
         const int* table = p.page_table + (long long)s.b * p.P;
 #pragma unroll 1
@@ -387,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
             }
             pending = slot;
           }
+          if (ok && t == s.t0) load_q();
         }
         at += s.t1 - s.t0;
       }
