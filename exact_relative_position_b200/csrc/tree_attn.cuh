@@ -342,56 +342,72 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   // ---- loads: rows of the cache by page, nodes behind them (16-bit cache)
   const uint8_t* kc_base = static_cast<const uint8_t*>(p.c.k);
   const uint8_t* vc_base = static_cast<const uint8_t*>(p.c.v);
-  constexpr int LR = (KW + 31) / 32;                    // rows whose place a lane looks up
-  auto lookup = [&](const Place& c, uint32_t (&at)[LR]) {
-    // row of the cache of the group's key 32 i + lane; all ones: none
-#pragma unroll
-    for (int i = 0; i < LR; ++i) {
-      const int lr = 32 * i + lane, j = c.tile * TK + wn * KW + lr;
-      at[i] = 0xffffffffu;
-      if (lr < KW && c.at < my_end && j < c.len) {
-        const int id = __ldg(p.page_table + (long long)c.b * p.P + (j >> p.c.page_shift));
-        if (id >= 0 && id < p.c.num_pages)
-          at[i] = (((uint32_t)id * (uint32_t)p.c.Hkv + (uint32_t)c.hkv) << p.c.page_shift) + (uint32_t)(j & page_mask);
-      }
+  // A group's KW keys lie in one page where pages are that large: one look-up, and
+  // all addresses are constants away from the first row's.
+  const bool one_page = KW <= page_mask + 1;
+  // row of the cache of key j; all ones: none
+  auto place_of = [&](const Place& c, int j) {
+    uint32_t at = 0xffffffffu;
+    if (j < c.len) {
+      const int id = __ldg(p.page_table + (long long)c.b * p.P + (j >> p.c.page_shift));
+      if (id >= 0 && id < p.c.num_pages)
+        at = (((uint32_t)id * (uint32_t)p.c.Hkv + (uint32_t)c.hkv) << p.c.page_shift) + (uint32_t)(j & page_mask);
     }
+    return at;
   };
-  auto issue = [&](const Place& c, int stage, const uint32_t (&at)[LR]) {
+  // ahead of the loads: the row of the group's first key
+  auto lookup = [&](const Place& c) { return c.at < my_end && one_page ? place_of(c, c.tile * TK + wn * KW) : 0xffffffffu; };
+  constexpr int LR = (KW + 31) / 32;                    // rows whose place a lane looks up otherwise
+  // returns whether all KW keys are valid cached ones
+  auto issue = [&](const Place& c, int stage, uint32_t first) {
     const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
     const int k0 = c.tile * TK + wn * KW;
-    const bool nodes = WIDE && k0 + KW > c.len;         // some rows are nodes, or past the end
-    bool all = true;
+    const int ch = gtid % CPR, r0 = gtid / CPR;
+    constexpr int RI = GT / CPR;                        // rows of an iteration
+    if (first != 0xffffffffu && k0 + KW <= c.len) {
+      const unsigned long long off = ((unsigned long long)first + r0) * (D * ES) + ch * 16;
+      const uint8_t *ksrc = kc_base + off, *vsrc = vc_base + off;
 #pragma unroll
-    for (int i = 0; i < LR; ++i) all = all && (at[i] != 0xffffffffu || 32 * i + lane >= KW);
-    if (__all_sync(0xffffffffu, all)) {                 // nearly every tile: nothing to check row by row
-      const int ch = gtid % CPR;
-      const uint8_t *ksrc = kc_base + ch * 16, *vsrc = vc_base + ch * 16;
-#pragma unroll
-      for (int i = 0; i < KW * CPR / GT; ++i) {
-        const int r = i * (GT / CPR) + gtid / CPR;
-        const uint32_t at_r = __shfl_sync(0xffffffffu, at[(LR > 1) ? (i * GT / CPR) / 32 : 0], r & 31);
-        const unsigned long long off = (unsigned long long)at_r * (D * ES);
-        cp_async16(sk + chunk_at<CPR, WIDE, false>(r, ch), ksrc + off);
-        cp_async16(sv + chunk_at<CPR, WIDE, true>(r, ch), vsrc + off);
+      for (int i = 0; i < KW / RI; ++i) {
+        cp_async16(sk + chunk_at<CPR, WIDE, false>(i * RI + r0, ch), ksrc + i * RI * D * ES);
+        cp_async16(sv + chunk_at<CPR, WIDE, true>(i * RI + r0, ch), vsrc + i * RI * D * ES);
       }
-      if (wm == 0) {
+      if (!WIDE && wm == 0) {
 #pragma unroll
         for (int i = 0; i < LR; ++i) {
           const int lr = 32 * i + lane;
-          if (lane == 0) valid_bits[wn][stage][i] = KW >= 32 ? 0xffffffffu : (1u << (KW & 31)) - 1u;
-          if (!WIDE && lr < KW) {
-            const uint32_t ss = sk + 2 * HALF + lr * 4;
-            cp_async4(ss, p.c.ks + at[i], 4);
-            cp_async4(ss + KW * 4, p.c.vs + at[i], 4);
+          if (KW % 32 == 0 || lr < KW) {
+            cp_async4(sk + 2 * HALF + lr * 4, p.c.ks + first + lr, 4);
+            cp_async4(sk + 2 * HALF + KW * 4 + lr * 4, p.c.vs + first + lr, 4);
           }
         }
       }
-      return;
+      return true;
     }
+    // row by row: small or missing pages, the end of the cache, and (16-bit cache) the nodes behind it
+    uint32_t at[LR];
+    const bool nodes = WIDE && k0 + KW > c.len;
+    bool all = !nodes;
 #pragma unroll
-    for (int i = 0; i < KW * CPR / GT; ++i) {
-      const int ci = i * GT + gtid, r = ci / CPR, ch = ci % CPR;
-      const uint32_t at_r = __shfl_sync(0xffffffffu, at[(LR > 1) ? (i * GT / CPR) / 32 : 0], r & 31);
+    for (int i = 0; i < LR; ++i) {
+      const int lr = 32 * i + lane;
+      at[i] = lr < KW ? place_of(c, k0 + lr) : 0xffffffffu;
+      all = all && (at[i] != 0xffffffffu || lr >= KW);
+      const bool ok = at[i] != 0xffffffffu || (nodes && lr < KW && k0 + lr >= c.len && k0 + lr < c.len + p.T);
+      const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+      if (wm == 0 && lane == 0) valid_bits[wn][stage][i] = bits;
+      if (!WIDE && wm == 0 && lr < KW) {
+        const uint32_t ss = sk + 2 * HALF + lr * 4;
+        const uint32_t src = ok ? at[i] : 0u;
+        cp_async4(ss, p.c.ks + src, ok ? 4 : 0);
+        cp_async4(ss + KW * 4, p.c.vs + src, ok ? 4 : 0);
+      }
+    }
+#pragma unroll 2
+    for (int i = 0; i < KW / RI; ++i) {
+      const int r = i * RI + r0;
+      const uint32_t mine = LR > 1 && i * RI >= 32 ? at[LR - 1] : at[0];
+      const uint32_t at_r = __shfl_sync(0xffffffffu, mine, r & 31);
       const uint8_t *ksrc = kc_base, *vsrc = vc_base;
       int bytes = 0;
       if (at_r != 0xffffffffu) {
@@ -410,43 +426,34 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       cp_async16(sk + chunk_at<CPR, WIDE, false>(r, ch), ksrc, bytes);
       cp_async16(sv + chunk_at<CPR, WIDE, true>(r, ch), vsrc, bytes);
     }
-#pragma unroll
-    for (int i = 0; i < LR; ++i) {
-      const int lr = 32 * i + lane;
-      bool ok = at[i] != 0xffffffffu;
-      if (nodes) ok = ok || (lr < KW && k0 + lr >= c.len && k0 + lr < c.len + p.T);
-      const uint32_t bits = __ballot_sync(0xffffffffu, ok);
-      if (wm == 0 && lane == 0) valid_bits[wn][stage][i] = bits;
-      if (!WIDE && wm == 0 && lr < KW) {
-        const uint32_t ss = sk + 2 * HALF + lr * 4;
-        const uint32_t src = ok ? at[i] : 0u;
-        cp_async4(ss, p.c.ks + src, ok ? 4 : 0);
-        cp_async4(ss + KW * 4, p.c.vs + src, ok ? 4 : 0);
-      }
-    }
+    return (bool)__all_sync(0xffffffffu, all);
   };
 
   Place ld, cp;
   ld.at = my_start;
   seat(ld);
   cp = ld;
-  uint32_t at_next[LR];
+  uint32_t at_next, full_stages = 0;                    // bit s: stage s holds KW valid cached keys
+  auto load = [&](int s, uint32_t first) {
+    bool full = false;
+    if (ld.at < my_end) full = issue(ld, s, first);
+    cp_async_commit();
+    full_stages = (full_stages & ~(1u << s)) | ((full ? 1u : 0u) << s);
+    advance(ld, 1);
+  };
   {
-    uint32_t at[TL::STAGES - 1][LR];
+    uint32_t at[TL::STAGES - 1];
     Place c = ld;
 #pragma unroll
     for (int s = 0; s < TL::STAGES - 1; ++s) {          // all look-ups first: their latencies overlap
-      lookup(c, at[s]);
+      at[s] = lookup(c);
       advance(c, 1);
     }
-    lookup(c, at_next);
-#pragma unroll
-    for (int s = 0; s < TL::STAGES - 1; ++s) {
-      if (ld.at < my_end) issue(ld, s, at[s]);
-      cp_async_commit();
-      advance(ld, 1);
-    }
+    at_next = lookup(c);
+#pragma unroll 1
+    for (int s = 0; s < TL::STAGES - 1; ++s) load(s, s == 0 ? at[0] : at[TL::STAGES - 2]);
   }
+  static_assert(TL::STAGES <= 3, "the first look-ups are picked from two");
   int stage = 0;
   // what ran before this kernel has been waited for by the relation kernel, where
   // there is one; its own results are read from here on
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 
     // One step of SK keys from key ko of the group's KW, staged at sk / sv.  EASY: every
     // key is a valid cached one, and its relation term saturated (or there is none).
-    auto step = [&](auto easy, int k0, int ko, uint32_t sk, uint32_t sv, int stage) {
+    auto step = [&](auto easy, int k0, int ko, uint32_t sk, uint32_t sv, int stage, bool full) {
       constexpr bool EASY = decltype(easy)::value;
       float s[NR][SG][4];
 #pragma unroll
@@ -665,7 +672,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
               }
           }
       }
-      if (!EASY) {
+      if (!EASY && !full) {
 #pragma unroll
         for (int g = 0; g < SG; ++g)
 #pragma unroll
@@ -777,24 +784,20 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       {
         int ns = stage + TL::STAGES - 1;
         if (ns >= TL::STAGES) ns -= TL::STAGES;
-        if (ld.at < my_end) issue(ld, ns, at_next);
-        cp_async_commit();
-        advance(ld, 1);
-        lookup(ld, at_next);
+        load(ns, at_next);
+        at_next = lookup(ld);
       }
       const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
       const int k0 = tile * TK + wn * KW;
-      bool easy = k0 + KW <= len && (!p.z || k0 + KW - 1 - len <= p.e_lo);
-#pragma unroll
-      for (int i = 0; i < LR; ++i)
-        easy = easy && valid_bits[wn][stage][i] == (KW >= 32 ? 0xffffffffu : (1u << (KW & 31)) - 1u);
+      const bool full = (full_stages >> stage) & 1u;
+      const bool easy = full && (!p.z || k0 + KW - 1 - len <= p.e_lo);
       if (easy) {
 #pragma unroll 1
-        for (int ko = 0; ko < KW; ko += TL::SK) step(std::true_type{}, k0, ko, sk, sv, stage);
+        for (int ko = 0; ko < KW; ko += TL::SK) step(std::true_type{}, k0, ko, sk, sv, stage, true);
       } else {
 #pragma unroll 1
         for (int ko = 0; ko < KW; ko += TL::SK)
-          if (k0 + ko < len + (WIDE ? p.T : 0)) step(std::false_type{}, k0, ko, sk, sv, stage);
+          if (k0 + ko < len + (WIDE ? p.T : 0)) step(std::false_type{}, k0, ko, sk, sv, stage, full);
       }
       if (++stage == TL::STAGES) stage = 0;
     }

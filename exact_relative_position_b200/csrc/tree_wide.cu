@@ -558,6 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
             }
           }
         }
+        if (whole && empty) {                           // not 0 times it: a padding query may hold anything
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
         if (row_ok) {
           float* dst = whole ? static_cast<float*>(p.o) + out_row * D + c : slot + (long long)(g * 128 + r) * D + c;
           if (whole && !p.o_f32) {
