@@ -585,9 +585,33 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       }
     };
 
+    // Unsaturated relation terms of a step's scores: looked up a step ahead where
+    // the registers for it are there (up to 16 rows to a warp)
+    struct Terms {
+      float v[NR][SG][4];
+    };
+    constexpr bool AHEAD = NR <= 2;
+    auto terms_of = [&](int kf, Terms& z) {             // kf: the step's first key
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float* zr = row_z[row_of(n, e)] - p.e_lo;
+          const int depth = row_depth[row_of(n, e)];
+#pragma unroll
+          for (int g = 0; g < SG; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              int at = kf + 16 * g + key0 + 2 * j - len;
+              if (WIDE && at >= 0) at = at < p.T ? node_depth[at] : 0;
+              z.v[n][g][2 * j + e] = zr[iclamp(at - depth, p.e_lo, p.e_hi)];
+            }
+        }
+    };
+
     // One step of SK keys from key ko of the group's KW, staged at sk / sv.  EASY: every
     // key is a valid cached one, and its relation term saturated (or there is none).
-    auto step = [&](auto easy, int k0, int ko, uint32_t sk, uint32_t sv, int stage, bool full) {
+    auto step = [&](auto easy, int k0, int ko, uint32_t sk, uint32_t sv, int stage, bool full, const Terms& z) {
       constexpr bool EASY = decltype(easy)::value;
       float s[NR][SG][4];
 #pragma unroll
@@ -596,24 +620,6 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         for (int g = 0; g < SG; ++g)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[n][g][i] = WIDE && EASY ? zlow[n][i & 1] : 0.f;
-      float z[NR][SG][4];                               // loaded before the MMAs, added after them
-      if (!EASY && p.z) {
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float* zr = row_z[row_of(n, e)] - p.e_lo;
-            const int depth = row_depth[row_of(n, e)];
-#pragma unroll
-            for (int g = 0; g < SG; ++g)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                int at = k0 + ko + 16 * g + key0 + 2 * j - len;
-                if (WIDE && at >= 0) at = at < p.T ? node_depth[at] : 0;
-                z[n][g][2 * j + e] = zr[iclamp(at - depth, p.e_lo, p.e_hi)];
-              }
-          }
-      }
       // ---- scores: k steps outside, so that consecutive MMAs have their own sums
 #pragma unroll
       for (int u = 0; u < CPR / 4; ++u) {
@@ -648,7 +654,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 #pragma unroll
           for (int g = 0; g < SG; ++g)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][g][i] += z[n][g][i];
+            for (int i = 0; i < 4; ++i) s[n][g][i] += z.v[n][g][i];
       }
       float rsv[SG][2];                                 // 1 / value scale of the thread's keys
       if (!WIDE) {
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
               for (int e = 0; e < 2; ++e) {
                 float& x = s[n][g][2 * j + e];
                 if (EASY) x = fmaf(x, kcol, lg + zlow[n][e]);
-                else x = fmaf(x, kcol, p.z ? lg + z[n][g][2 * j + e] : lg);
+                else x = fmaf(x, kcol, p.z ? lg + z.v[n][g][2 * j + e] : lg);
               }
           }
       }
@@ -777,6 +783,9 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       if (WIDE && !EASY && __any_sync(0xffffffffu, odd)) add_non_finite(k0 + ko - len, k0 + ko + TL::SK - len);
     };
 
+    Terms z_next;
+    auto unsaturated = [&](int kf) { return p.z && kf + TL::SK - 1 - len > p.e_lo; };
+    if (AHEAD && unsaturated(tile0 * TK + wn * KW)) terms_of(tile0 * TK + wn * KW, z_next);
 #pragma unroll 1
     for (int tile = tile0; tile < tile1; ++tile) {
       cp_async_wait<TL::STAGES - 2>();
@@ -790,14 +799,24 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
       const int k0 = tile * TK + wn * KW;
       const bool full = (full_stages >> stage) & 1u;
-      const bool easy = full && (!p.z || k0 + KW - 1 - len <= p.e_lo);
-      if (easy) {
 #pragma unroll 1
-        for (int ko = 0; ko < KW; ko += TL::SK) step(std::true_type{}, k0, ko, sk, sv, stage, true);
-      } else {
-#pragma unroll 1
-        for (int ko = 0; ko < KW; ko += TL::SK)
-          if (k0 + ko < len + (WIDE ? p.T : 0)) step(std::false_type{}, k0, ko, sk, sv, stage, full);
+      for (int ko = 0; ko < KW; ko += TL::SK) {
+        if (full && !unsaturated(k0 + ko)) {
+          step(std::true_type{}, k0, ko, sk, sv, stage, true, z_next);
+        } else if (k0 + ko < len + (WIDE ? p.T : 0)) {
+          Terms z = z_next;
+          if (p.z && (!AHEAD || !unsaturated(k0 + ko))) terms_of(k0 + ko, z);   // (a missing page among saturated keys)
+          if (AHEAD) {
+            const int kn = ko + TL::SK < KW ? k0 + ko + TL::SK : k0 + TK;
+            if (unsaturated(kn)) terms_of(kn, z_next);
+          }
+          step(std::false_type{}, k0, ko, sk, sv, stage, full, z);
+          continue;
+        }
+        if (AHEAD) {
+          const int kn = ko + TL::SK < KW ? k0 + ko + TL::SK : k0 + TK;
+          if (unsaturated(kn)) terms_of(kn, z_next);
+        }
       }
       if (++stage == TL::STAGES) stage = 0;
     }

@@ -73,7 +73,7 @@ def _launch(name, dev, *args):
 
 
 def _cuda(name, t, dtype, dev):
-    if t.device != dev or t.dtype is not dtype:
+    if t.dtype is not dtype or t.get_device() != dev.index:
         raise RelPosError(f"{name} must be a CUDA tensor of {dtype} on {dev}")
 
 
@@ -420,23 +420,27 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     Calls that may overlap on the GPU need workspaces of their own; by default each
     call takes its own from PyTorch's allocator."""
     dev, dt = cache.device, q.dtype
-    if dt not in (torch.float16, torch.bfloat16) or (not cache.coded and dt != cache.dtype):
+    index = dev.index
+    if dt not in (torch.float16, torch.bfloat16) or (not cache.coded and dt is not cache.dtype):
         raise RelPosError(f"q of {dt} does not go with a cache of {cache.dtype}")
-    _cuda("q", q, dt, dev)
-    (B, H, T, d), qs = _view("q", q, packed_ok=False)
+    if q.get_device() != index or k.get_device() != index or v.get_device() != index or k.dtype is not dt or v.dtype is not dt:
+        raise RelPosError(f"q, k and v must be CUDA tensors of one type on {dev}")
+    if q.dim() != 4:
+        raise RelPosError("q must be [B, H, T, d]")
+    B, H, T, d = q.shape
     Hkv = cache.kv_heads
     if d != cache.d or d not in (64, 128) or H % Hkv:
         raise RelPosError("q must have the cache's head dimension (64 or 128) and a multiple of its heads")
     if not 1 <= T <= MAX_NODES:
         raise RelPosError(f"1 to {MAX_NODES} drafted tokens")
-    _cuda("k", k, dt, dev)
-    _cuda("v", v, dt, dev)
     if k.shape != (B, Hkv, T, d) or v.shape != k.shape:
         raise RelPosError("k and v must be [B, kv_heads, T, d]")
-    if q.stride(-1) != 1 or k.stride(-1) != 1 or v.stride(-1) != 1:
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if qs[3] != 1 or ks[3] != 1 or vs[3] != 1:
         raise RelPosError("the last dimension of q, k and v must be contiguous")
-    _cuda("page_table", page_table, torch.int32, dev)
-    _cuda("lengths", lengths, torch.int32, dev)
+    if page_table.dtype is not torch.int32 or lengths.dtype is not torch.int32 or page_table.get_device() != index \
+            or lengths.get_device() != index:
+        raise RelPosError(f"page_table and lengths must be int32 on {dev}")
     if page_table.dim() != 2 or page_table.shape[0] != B or lengths.shape != (B,) \
             or not page_table.is_contiguous() or not lengths.is_contiguous():
         raise RelPosError("page_table must be contiguous [B, P] and lengths [B]")
@@ -469,7 +473,7 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
             if b.shape != (H, R) or not b.is_contiguous():
                 raise RelPosError(f"b must be contiguous float32 [{H}, {R}]")
     if o is None:
-        o = torch.empty((B, H, T, d), device=dev, dtype=torch.float32 if out_f32 else dt)
+        o = torch.empty_like(q, dtype=torch.float32 if out_f32 else None, memory_format=torch.contiguous_format)
     elif o.shape != q.shape or not o.is_contiguous() or o.dtype != (torch.float32 if out_f32 else dt) or o.device != dev:
         raise RelPosError("o must be contiguous, shaped like q, of the output's dtype")
     if lse is None:
@@ -485,8 +489,8 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     elif workspace.device != dev or not workspace.is_contiguous():
         raise RelPosError(f"workspace must be contiguous on {dev}")
     a = _TREE.pack(*cache._fields, B, T, H, 0, code, F32 if out_f32 else code, tau, N, P, per_head, *desc, per_seq,
-                   page_table.data_ptr(), lengths.data_ptr(), mask_ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs,
-                   *k.stride()[:3], *v.stride()[:3], 0 if aq is None else aq.data_ptr(),
+                   page_table.data_ptr(), lengths.data_ptr(), mask_ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0],
+                   qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], 0 if aq is None else aq.data_ptr(),
                    0 if b is None else b.data_ptr(), o.data_ptr(), lse.data_ptr())
     _launch("relpos_tree_attn", dev, a, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return o, lse

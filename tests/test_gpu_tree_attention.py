@@ -215,6 +215,18 @@ def test_non_finite_in_masked_places(dt, fmt, val, H):
     assert bool((~torch.isfinite(o[:, :, 3, 5])).all())
 
 
+@pytest.mark.parametrize("H,T", [(2, 2), (4, 7), (4, 12), (8, 40)])
+def test_bad_pages_far_from_the_queries(H, T):
+    # a missing page among keys whose relation terms are saturated, and one among the others
+    for fmt in (F16, INT8):
+        s = make(B=2, H=H, Hkv=2, T=T, lens=[900, 700], fmt=fmt, page=16, map=rp.RelPosMap("truncated", clip=20), aq="head", b=True,
+                 tree="tree")
+        s["table"][0, 10] = -1
+        s["table"][0, 55] = 10 ** 6
+        s["table"][1, 0] = s["cache"].num_pages
+        check_tree(call(s), want(s), F16)
+
+
 def test_bad_pages_are_masked():
     for fmt in (F16, INT8):
         s = make(B=2, H=2, Hkv=2, T=2, lens=[100, 64], fmt=fmt, page=16)
