@@ -840,8 +840,6 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
   if (!(a->tau > 0.f) || a->tau > 3.0e38f) return RELPOS_ERR_INVALID_ARG;
   const long long cap = (long long)a->pages_per_seq * a->cache.page_size;
   if (cap > (1LL << 30)) return RELPOS_ERR_INVALID_ARG;
-  // tiles are counted in 32 bits
-  if ((cap / 32 + 4) * a->B > 0x7fffffffLL) return RELPOS_ERR_INVALID_ARG;
   p->B = a->B; p->T = a->T; p->H = a->H; p->G = a->H / a->cache.kv_heads;
   p->bf16 = a->dtype == RELPOS_BF16;
   p->o_f32 = a->out_dtype == RELPOS_F32;
@@ -886,7 +884,8 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
   const int rows = p->G * a->T;
   p->rows_per_block = tree_rows_per_block(*p);
   p->row_blocks = (rows + p->rows_per_block - 1) / p->rows_per_block;
-  if ((long long)a->B * a->cache.kv_heads * p->row_blocks > 0x7fffffffLL) return RELPOS_ERR_INVALID_ARG;
+  // tiles (of 64 keys at least) are counted in 31 bits, and the next piece's start with them
+  if ((cap / 64 + 4) * a->B * a->cache.kv_heads * p->row_blocks > 0x3fffffffLL) return RELPOS_ERR_INVALID_ARG;
   p->grid = tree_grid(*p);
   L->part = take(sizeof(float) * 2 * (size_t)p->grid * (size_t)p->rows_per_block * (a->cache.d + 2));
   {

@@ -105,16 +105,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   line.pre = pre;
   line.B = p.B;
   line.items = p.c.Hkv * p.row_blocks;
-  line.total = (long long)pre[p.B] * line.items;
+  line.total = pre[p.B] * line.items;
   line.quantum = (line.total + p.grid - 1) / p.grid;
-  const long long at = line.quantum * (blockIdx.x + 1);
+  const int at = line.quantum * (int)(blockIdx.x + 1);
   const int b = line.seq_of(min(at, line.total - 1));
   const int nt = pre[b + 1] - pre[b];
-  const long long in_b = at - (long long)pre[b] * line.items;
-  const int item = (int)(in_b / nt), tile = (int)(in_b - (long long)item * nt);
-  const long long start = at - tile, before = line.quantum * blockIdx.x;
+  const int in_b = at - pre[b] * line.items, item = in_b / nt, tile = in_b - item * nt;
+  const int start = at - tile, before = line.quantum * blockIdx.x;
   const bool mine = at < line.total && tile > 0 && start >= before;
-  const int c0 = blockIdx.x, c1 = (int)((start + nt - 1) / line.quantum);
+  const int c0 = blockIdx.x, c1 = (start + nt - 1) / line.quantum;
   const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
   const int n = min(ROWS, p.G * p.T - rb * ROWS);
   // every block waits, the idle ones too: what follows this kernel on the stream
@@ -230,7 +229,7 @@ cudaError_t launch_tree_relation(const TreeParams& p, cudaStream_t s) {
   } else {
     const int row_tiles = (p.B * p.T + 15) / 16, cols = (W + 63) / 64;
     // walk the query rows in one block where the columns alone fill the card
-    int gz = (int)(148LL * 8 / ((long long)cols * p.H)) + 1;
+    int gz = (int)(148LL * 32 / ((long long)cols * p.H)) + 1;
     gz = gz < row_tiles ? gz : row_tiles;
     const dim3 grid(cols, p.H, gz);
     if (p.c.d == 64) {

@@ -93,12 +93,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 struct Line {
   const int* pre;
   int B, items;                      // items (key head, row block) of a sequence
-  long long total, quantum;
-  __device__ __forceinline__ int seq_of(long long at) const {
+  int total, quantum;                // tiles of the line and of a piece
+  __device__ __forceinline__ int seq_of(int at) const {
     int lo = 0, hi = B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)pre[mid] * items <= at) lo = mid; else hi = mid;
+      if (pre[mid] * items <= at) lo = mid; else hi = mid;
     }
     return lo;
   }
@@ -302,10 +302,10 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   line.pre = pre;
   line.B = p.B;
   line.items = p.c.Hkv * p.row_blocks;
-  line.total = (long long)pre[p.B] * line.items;
+  line.total = pre[p.B] * line.items;
   line.quantum = (line.total + gridDim.x - 1) / gridDim.x;
-  const long long my_start = line.quantum * blockIdx.x;
-  const long long my_end = min(line.total, my_start + line.quantum);
+  const int my_start = line.quantum * blockIdx.x;
+  const int my_end = min(line.total, my_start + line.quantum);
   if (my_start >= my_end) return;
   const int page_mask = (1 << p.c.page_shift) - 1;
   const int R = p.G * p.T;
@@ -313,15 +313,14 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   // Two places on the line: the tile that is loaded next and the one that is
   // computed.  Loads run ahead across the borders of items.
   struct Place {
-    long long at;
-    int b, item, tile, nt, len, hkv;
+    int at, b, item, tile, nt, len, hkv;
   };
   auto seat = [&](Place& c) {
     c.b = line.seq_of(c.at);
     c.nt = pre[c.b + 1] - pre[c.b];
-    const long long in_b = c.at - (long long)pre[c.b] * line.items;
-    c.item = (int)(in_b / c.nt);
-    c.tile = (int)(in_b - (long long)c.item * c.nt);
+    const int in_b = c.at - pre[c.b] * line.items;
+    c.item = in_b / c.nt;
+    c.tile = in_b - c.item * c.nt;
     c.hkv = c.item / p.row_blocks;
     c.len = seq_len(p, c.b);
   };
@@ -463,7 +462,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   while (cp.at < my_end) {
     const int b = cp.b, nt = cp.nt, hkv = cp.hkv, len = cp.len;
     const int rb = cp.item - hkv * p.row_blocks;
-    const int tile0 = cp.tile, tile1 = (int)min((long long)nt, tile0 + (my_end - cp.at));
+    const int tile0 = cp.tile, tile1 = min(nt, tile0 + (my_end - cp.at));
     const bool first_item = cp.at == my_start;
 
     // ---- the rows of the item
@@ -1072,16 +1071,16 @@ cudaError_t run_tiling(const TreeParams& p, cudaStream_t s) {
 // to an SM with some 100 KB of loads in flight.
 template <int D, bool WIDE> struct Tilings;
 template <bool WIDE> struct Tilings<64, WIDE> {
-  using R8 = Tiling<64, 1, 4, 1, WIDE ? 16 : 32, 16, 3, 4>;
-  using R16 = Tiling<64, 1, 4, 2, WIDE ? 16 : 32, 16, 3, 4>;
-  using R32 = Tiling<64, 1, 4, 4, WIDE ? 16 : 32, 16, 3, 3>;
-  using R64 = Tiling<64, 2, 2, 4, 32, 16, 3, 3>;
+  using R8 = Tiling<64, 1, 4, 1, 32, 32, WIDE ? 2 : 3, WIDE ? 3 : 4>;
+  using R16 = Tiling<64, 1, 4, 2, WIDE ? 16 : 32, WIDE ? 16 : 32, 3, 3>;
+  using R32 = Tiling<64, 2, 2, 2, 32, WIDE ? 16 : 32, 3, 3>;
+  using R64 = Tiling<64, 4, 1, 2, 64, 32, 3, 3>;
 };
 template <bool WIDE> struct Tilings<128, WIDE> {
-  using R8 = Tiling<128, 1, 4, 1, 16, 16, 3, WIDE ? 2 : 4>;
+  using R8 = Tiling<128, 1, 4, 1, WIDE ? 16 : 32, WIDE ? 16 : 32, WIDE ? 3 : 2, WIDE ? 2 : 3>;
   using R16 = Tiling<128, 1, 4, 2, 16, 16, 3, WIDE ? 2 : 3>;
-  using R32 = Tiling<128, 2, 2, 2, 32, 16, 3, WIDE ? 2 : 3>;
-  using R64 = Tiling<128, 4, 1, 2, 64, 16, 3, WIDE ? 2 : 3>;
+  using R32 = Tiling<128, 2, 2, 2, 32, 16, 3, 2>;
+  using R64 = Tiling<128, 4, 1, 2, 64, 32, 3, 2>;
 };
 
 template <typename QT, int FMT, class T>

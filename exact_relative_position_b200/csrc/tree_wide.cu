@@ -129,24 +129,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
   line.pre = pre;
   line.B = p.B;
   line.items = p.c.Hkv * p.row_blocks;
-  line.total = (long long)pre[p.B] * line.items;
+  line.total = pre[p.B] * line.items;
   line.quantum = (line.total + gridDim.x - 1) / gridDim.x;
-  const long long my_start = line.quantum * blockIdx.x;
-  const long long my_end = min(line.total, my_start + line.quantum);
+  const int my_start = line.quantum * blockIdx.x;
+  const int my_end = min(line.total, my_start + line.quantum);
   const int R = p.G * p.T;
 
   // the piece's part of one item: tiles [t0, t1) of nt
   struct Seg {
     int b, hkv, rb, nt, t0, t1, len, groups;
   };
-  auto segment = [&](long long at) {
+  auto segment = [&](int at) {
     Seg s;
     s.b = line.seq_of(at);
     s.nt = pre[s.b + 1] - pre[s.b];
-    const long long in_b = at - (long long)pre[s.b] * line.items;
-    const int item = (int)(in_b / s.nt);
-    s.t0 = (int)(in_b - (long long)item * s.nt);
-    s.t1 = (int)min((long long)s.nt, s.t0 + (my_end - at));
+    const int in_b = at - pre[s.b] * line.items, item = in_b / s.nt;
+    s.t0 = in_b - item * s.nt;
+    s.t1 = min(s.nt, s.t0 + (my_end - at));
     s.hkv = item / p.row_blocks;
     s.rb = item - s.hkv * p.row_blocks;
     s.len = seq_len(p, s.b);
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         uint32_t unit = 0, seg_no = 0, np[2] = {0, 0};
         auto full = [&](uint32_t u) { return mbar_wait(bar(kBarFull + u % W::kUnits), (u / W::kUnits) & 1, abort_flag, limit); };
         bool ok = true;
-        for (long long at = my_start; at < my_end && ok; ++seg_no) {
+        for (int at = my_start; at < my_end && ok; ++seg_no) {
           const Seg s = segment(at);
           const int n = s.t1 - s.t0;
           ok = mbar_wait(bar(kBarQFull), seg_no & 1, abort_flag, limit) && full(unit);
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         return (bool)__all_sync(0xffffffffu, got);
       };
       bool ok = true;
-      for (long long at = my_start; at < my_end && ok; ++seg_no) {
+      for (int at = my_start; at < my_end && ok; ++seg_no) {
         const Seg s = segment(at);
         // ---- queries, 32 rows to a warp in turn, once the first tiles are under way
         auto load_q = [&]() {
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
     bool ok = true;
     // the relation terms are read, and results written, from here on
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (long long at = my_start; at < my_end && ok; ++seg_no) {
+    for (int at = my_start; at < my_end && ok; ++seg_no) {
       const Seg s = segment(at);
       const int n = s.t1 - s.t0;
       if (g >= s.groups) {
