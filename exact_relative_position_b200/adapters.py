@@ -24,7 +24,7 @@ import math
 
 import torch
 
-from . import RelPosMap, relpos_attention
+from . import RelPosMap, relpos_attention, relpos_tree_attention
 
 
 def sinusoid_table(N: int, dim: int, device=None) -> torch.Tensor:
@@ -72,6 +72,22 @@ class TransformerXLRelPos(torch.nn.Module):
         qp, aq, b = self.unified_inputs(q)
         return relpos_attention(qp, k, v, aq, None, b, tau=self.tau, map=RelPosMap("identity"), causal=self.causal,
                                 projection=self.projection)
+
+    @torch.no_grad()
+    def decode_tables(self, max_seqlen: int, dtype: torch.dtype):
+        """(aQ, b) of unified_inputs for sequences up to max_seqlen, to be kept over a generation."""
+        _, aq, b = self.unified_inputs(torch.zeros(1, 1, max_seqlen, self.d_head, device=self.u.device, dtype=dtype))
+        return aq, b
+
+    @torch.no_grad()
+    def decode(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache, page_table, lengths, tables,
+               tree_mask=None) -> torch.Tensor:
+        """The causal layer's rows of T drafted tokens (q, k, v [B, H, T, d_head]) behind `lengths` cached ones;
+        tables as decode_tables gives them, tree_mask as relpos_tree_attention takes it."""
+        aq, b = tables
+        qp = q + self.u[None, :, None, :].to(q.dtype)
+        return relpos_tree_attention(qp, k, v, cache, page_table, lengths, aq, b, tau=self.tau, map=RelPosMap("identity"),
+                                     tree_mask=tree_mask)[0]
 
 
 class DebertaRelPos(torch.nn.Module):

@@ -949,7 +949,7 @@ RELPOS_EXPORT int relpos_cache_write(const relpos_cache_write_args* a, relpos_st
   p.kst = strides(a->k_stride_b, a->k_stride_h, a->k_stride_n);
   p.vst = strides(a->v_stride_b, a->v_stride_h, a->v_stride_n);
   if (!rows16(p.kst) || !rows16(p.vst)) return RELPOS_ERR_INVALID_ARG;
-  if ((long long)a->B * a->N > (1LL << 31) / a->cache.kv_heads) return RELPOS_ERR_INVALID_ARG;
+  if ((long long)a->B * a->N >= (1LL << 31) / a->cache.kv_heads) return RELPOS_ERR_INVALID_ARG;
   p.B = a->B; p.N = a->N;
   p.slots = reinterpret_cast<const long long*>(a->slots);
   p.bf16 = a->dtype == RELPOS_BF16;

@@ -11,7 +11,10 @@
 // is rounded to the 24 bits of the sine's argument), at the cost of one 64-bit
 // multiply.
 //
-// Bound by memory: each element is read once and written once.
+// Bound by memory: each element is read once and written once.  A thread turns one
+// head at a time: blocks with more loads to a thread hold fewer threads and were
+// slower (4 x 4097 tokens of 40 heads of 128, both directions: 140 us, 4.8 TB/s, at one
+// head, 156 at four).
 #include "serve.cuh"
 #include "kernels.cuh"
 
@@ -38,15 +41,25 @@ template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
 
 // One thread: V frequencies of one token (two vectors of V elements), for up
 // to `hpt` heads, so that the sines are taken once for all of them.
-template <typename T, int V>
+template <typename T, int V, bool SMALL>
 __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryParams p, int pair_jobs,
                                                      int jobs, int hpt) {
   using VT = Vec<T, V>;
-  const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const int job = (int)(idx % jobs);
-  const long long tok = idx / jobs;
-  if (tok >= (long long)p.B * p.N) return;
-  const int b = (int)(tok / p.N), n = (int)(tok % p.N);
+  // 32-bit division where the counts allow it: one in 64 bits costs as much as turning a row
+  int job, b, n;
+  if (SMALL) {
+    const uint32_t idx = blockIdx.x * 256u + threadIdx.x, tok = idx / (uint32_t)jobs;
+    if (tok >= (uint32_t)p.B * (uint32_t)p.N) return;
+    job = (int)(idx - tok * jobs);
+    b = (int)(tok / (uint32_t)p.N);
+    n = (int)(tok - (uint32_t)b * p.N);
+  } else {
+    const long long idx = (long long)blockIdx.x * 256 + threadIdx.x, tok = idx / jobs;
+    if (tok >= (long long)p.B * p.N) return;
+    job = (int)(idx - tok * jobs);
+    b = (int)(tok / p.N);
+    n = (int)(tok - (long long)b * p.N);
+  }
 
   const bool turn = job < pair_jobs;
   float cs[V], sn[V];
@@ -77,7 +90,7 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
   }
   const int Ht = p.t[0].H + (p.n_tensors > 1 ? p.t[1].H : 0);
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Ht);
-#pragma unroll 4
+#pragma unroll 1
   for (int hh = h0; hh < h1; ++hh) {
     const RotaryTensor& t = hh < p.t[0].H ? p.t[0] : p.t[1];
     const int h = hh < p.t[0].H ? hh : hh - p.t[0].H;
@@ -128,12 +141,14 @@ cudaError_t go(const RotaryParams& p, cudaStream_t s) {
   const int jobs = pair_jobs + (p.d - p.rotary_dim + 2 * V - 1) / (2 * V);
   const int Ht = p.t[0].H + (p.n_tensors > 1 ? p.t[1].H : 0);
   const long long threads = (long long)p.B * p.N * jobs;
-  // heads a thread turns with one set of sines: as many as leave two blocks to an SM
+  // heads a thread turns with one set of sines: as many as leave two blocks to an SM, up to
+  // 8 (16 left too few threads: 151 us in place of 140)
   int hpt = (int)(threads * Ht / (148LL * 512));
   hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : hpt;
   const int hy = (Ht + hpt - 1) / hpt;
   dim3 grid((unsigned)((threads + 255) / 256), (unsigned)hy);
-  rotary_kernel<T, V><<<grid, 256, 0, s>>>(p, pair_jobs, jobs, hpt);
+  if (threads < (1LL << 31)) rotary_kernel<T, V, true><<<grid, 256, 0, s>>>(p, pair_jobs, jobs, hpt);
+  else rotary_kernel<T, V, false><<<grid, 256, 0, s>>>(p, pair_jobs, jobs, hpt);
   note_launch(1);
   return cudaGetLastError();
 }

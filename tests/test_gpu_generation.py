@@ -91,3 +91,21 @@ def test_rotary_trains_through_the_layer():
                                                      None, b, tau=0.125, map=m, causal=True), x, do)
     for got, up in ((gq, dq), (gk, dk)):
         assert torch.equal(got, rp.relpos_rotary(up, rotary=rot, inverse=True))
+
+
+def test_transformer_xl_layer_decodes_its_own_rows():
+    from exact_relative_position_b200.adapters import TransformerXLRelPos
+    torch.manual_seed(8)
+    H, N, d, prompt, page = 2, 75, 64, 60, 16
+    layer = TransformerXLRelPos(H, d, init_std=0.3).cuda()
+    q, k, v = (torch.randn(1, H, N, d, device="cuda").half() for _ in range(3))
+    with torch.no_grad():
+        full = layer(q, k, v)
+    cache = rp.kv_cache(-(-N // page), page, H, d, torch.float16)
+    table = torch.arange(cache.num_pages, dtype=torch.int32).flip(0)[None].contiguous().cuda()
+    slots = torch.tensor([[int(table[0, i // page]) * page + i % page for i in range(prompt)]]).cuda()
+    rp.kv_cache_write(cache, k[:, :, :prompt], v[:, :, :prompt], slots)
+    o = layer.decode(q[:, :, prompt:], k[:, :, prompt:], v[:, :, prompt:], cache, table,
+                     torch.tensor([prompt], dtype=torch.int32).cuda(), layer.decode_tables(N, torch.float16))
+    # both round P and O to fp16 (2 x 2^-11 of |v| < 6 a side)
+    assert float((o - full[:, :, prompt:]).abs().max()) <= 2 * 6 * 2.0 ** -10
