@@ -59,6 +59,11 @@ struct WideShared {
   int warp_sums[kThreads / 32];
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tma_rows_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int row) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
@@ -452,23 +457,49 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         if (!easy) {
           // masks and unsaturated relation terms, 32 keys at a time, back into tensor memory
           const float* zr = p.z ? z - p.e_lo : nullptr;
+          const int* sh_depth = sh.depth[g];
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             float y[32];
             tmem_ld32(tS + 32 * i, reinterpret_cast<uint32_t*>(y));
             tmem_wait_ld();
             const uint32_t bits = vw[i];
+            const int o0 = k0 + 32 * i - s.len, d0 = o0 - depth;   // from the end of the cache, and the offset, of column 0
+            if (p.z && o0 + 32 <= 0 && d0 + 31 <= p.e_lo) {
+              const float low = z[0];                   // saturated for this row
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              int o = k0 + 32 * i + c - s.len;          // node, or the offset from the end of the cache
-              bool keep = (bits >> c) & 1u;
-              if (o >= 0) {
-                keep = keep && ((mk >> (o & 63)) & 1ull);
-                o = sh.depth[g][o & 63];
+              for (int c = 0; c < 32; ++c) y[c] += low;
+            } else if (p.z && o0 + 32 <= 0 && d0 >= p.e_lo && d0 + 31 <= p.e_hi) {
+              // 32 consecutive terms: aligned groups of four (rows of z are padded to eight), turned by the rest.
+              // A ninth group is needed, and then lies in the row, unless the first starts on a group.
+              const int a = d0 - p.e_lo, sh = a & 3;
+              const float4* src = reinterpret_cast<const float4*>(z + (a & ~3));
+              float f[36];
+#pragma unroll
+              for (int c = 0; c < 9; ++c) {
+                const float4 w = c < 8 || sh ? __ldg(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                f[4 * c] = w.x; f[4 * c + 1] = w.y; f[4 * c + 2] = w.z; f[4 * c + 3] = w.w;
               }
-              if (p.z) y[c] += zr[iclamp(o - depth, p.e_lo, p.e_hi)];
-              if (!keep) y[c] = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < 35; ++c) f[c] = sh & 1 ? f[c + 1] : f[c];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) y[c] += sh & 2 ? f[c + 2] : f[c];
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                int o = o0 + c;                         // node, or the place from the end of the cache
+                if (o >= 0) o = sh_depth[o & 63];
+                if (p.z) y[c] += zr[iclamp(o - depth, p.e_lo, p.e_hi)];
+              }
             }
+            if (o0 + 32 > 0 || bits != 0xffffffffu) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const int o = o0 + c;
+                if (!((bits >> c) & 1u) || (o >= 0 && !((mk >> (o & 63)) & 1ull))) y[c] = -INFINITY;
+              }
+            }
+            __syncwarp();                               // the store is the whole warp's
             tmem_st32(tS + 32 * i, reinterpret_cast<uint32_t*>(y));
           }
           tmem_wait_st();
@@ -481,12 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         tmem_wait_ld();
         float pm[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) pm[u] = fmaxf(x[u], x[u + 8]);
+        for (int u = 0; u < 8; ++u) pm[u] = max3(x[u], x[u + 8], x[u + 16]);
 #pragma unroll
-        for (int c = 16; c < 128; c += 8)
+        for (int c = 24; c < 120; c += 16)
 #pragma unroll
-          for (int u = 0; u < 8; ++u) pm[u] = fmaxf(pm[u], x[c + u]);
-        const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+          for (int u = 0; u < 8; ++u) pm[u] = max3(pm[u], x[c + u], x[c + 8 + u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) pm[u] = fmaxf(pm[u], x[120 + u]);
+        const float mx = max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
         const float m_new = fmaxf(m_run, mx * c2 + rowc);
         const bool grow = m_new > m_run + kSlack;
         if (__any_sync(0xffffffffu, grow)) {
