@@ -265,8 +265,9 @@ def test_strides_outputs_and_streams():
         call(s, workspace=ws[:need // 2])
 
 
-def test_captured_graph_follows_its_buffers():
-    s = make(B=2, H=4, Hkv=2, T=3, lens=[200, 64], fmt=INT8, map=rp.RelPosMap("t5", num_buckets=32, max_distance=128, bidirectional=0), b=True)
+@pytest.mark.parametrize("fmt,H,T", [(INT8, 4, 3), (F16, 8, 20)])        # 6 rows; 80, the many-row kernel
+def test_captured_graph_follows_its_buffers(fmt, H, T):
+    s = make(B=2, H=H, Hkv=2, T=T, lens=[200, 64], fmt=fmt, map=rp.RelPosMap("t5", num_buckets=32, max_distance=128, bidirectional=0), b=True)
     s["table"].clamp_(min=0)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
@@ -282,6 +283,23 @@ def test_captured_graph_follows_its_buffers():
         g.replay()
         eager = call(s)
         assert torch.equal(o, eager[0]) and torch.equal(lse, eager[1])
+
+
+def test_calls_on_two_streams_at_once():
+    a = make(seed=1, B=3, H=8, Hkv=2, T=20, lens=[900, 1500, 3], tree="tree", map=rp.RelPosMap("truncated", clip=16), aq="head", b=True)
+    b = make(seed=2, B=5, H=4, Hkv=4, T=1, lens=[4000, 1, 77, 0, 900], fmt=E4M3, map=rp.RelPosMap("identity"), aq="shared")
+    want_a, want_b = call(a), call(b)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(10):
+        for s, st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                got.append((call(s), s is a))
+    torch.cuda.synchronize()
+    for (o, lse), first in got:
+        w = want_a if first else want_b
+        assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
 
 
 def test_refusals():
