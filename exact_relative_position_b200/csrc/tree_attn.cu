@@ -11,7 +11,15 @@ namespace {
 // offsets.  A warp keeps 16 table rows in registers and walks over the rows
 // of queries, so the table is read once; z is written in fp32.  Offsets that no
 // row of 16 can reach (they lie before position 0) are left out.
-template <int D, typename QT>
+// BUCKETS: the map takes logarithms; the others' code is short, and at this length
+// of kernel what the instruction caches must fetch shows.
+template <bool BUCKETS>
+__device__ __forceinline__ int row_at(const TreeParams& p, int delta) {
+  const int r = BUCKETS ? phi_of(p.map, p.N, delta)
+                        : p.map.kind == RELPOS_MAP_TRUNCATED ? iclamp(delta, -p.map.clip, p.map.clip) + p.map.clip : delta + p.N - 1;
+  return iclamp(r, 0, p.R - 1);
+}
+template <int D, typename QT, bool BUCKETS>
 __global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ TreeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, q4 = lane & 3, r8 = lane >> 2;
@@ -20,11 +28,11 @@ __global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ T
   if (c0 >= W) return;
   const int h = blockIdx.y;
   uint4 bw[2][D / 32];
+  int rows[2];                         // table rows of columns r8 and 8 + r8
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int c = min(c0 + 8 * j + r8, W - 1);
-    const int r = iclamp(phi_of(p.map, p.N, p.e_lo + c), 0, p.R - 1);
-    const uint16_t* src = static_cast<const uint16_t*>(p.aq) + h * p.aq_hs + (long long)r * D;
+    rows[j] = row_at<BUCKETS>(p, p.e_lo + min(c0 + 8 * j + r8, W - 1));
+    const uint16_t* src = static_cast<const uint16_t*>(p.aq) + h * p.aq_hs + (long long)rows[j] * D;
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) bw[j][u] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u + 8 * q4));
   }
@@ -34,18 +42,18 @@ __global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ T
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int col = min(c0 + 8 * j + 2 * q4 + c, W - 1);
-        bias[j][c] = p.bias[(long long)h * p.R + iclamp(phi_of(p.map, p.N, p.e_lo + col), 0, p.R - 1)];
+        const int r = __shfl_sync(0xffffffffu, rows[j], 4 * (2 * q4 + c));   // the row of this lane's column
+        bias[j][c] = p.bias[(long long)h * p.R + r];
       }
   }
-  const int rows = p.B * p.T;
-  for (int r0 = blockIdx.z * 16; r0 < rows; r0 += gridDim.z * 16) {
+  const int n = p.B * p.T;
+  for (int r0 = blockIdx.z * 16; r0 < n; r0 += gridDim.z * 16) {
     int rr[2], bb[2], tt[2];
     bool need = false;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       rr[e] = r0 + r8 + 8 * e;
-      const int r = min(rr[e], rows - 1);
+      const int r = min(rr[e], n - 1);
       bb[e] = r / p.T;
       tt[e] = r - bb[e] * p.T;
       need = need || p.e_lo + c0 + 15 >= -(seq_len(p, bb[e]) + p.T);
@@ -68,7 +76,7 @@ __global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ T
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (rr[e] >= rows) continue;
+      if (rr[e] >= n) continue;
       float* dst = p.z + bb[e] * p.z_b + h * p.z_h + tt[e] * p.z_t + c0 + 2 * q4;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -232,13 +240,14 @@ cudaError_t launch_tree_relation(const TreeParams& p, cudaStream_t s) {
     int gz = (int)(148LL * 32 / ((long long)cols * p.H)) + 1;
     gz = gz < row_tiles ? gz : row_tiles;
     const dim3 grid(cols, p.H, gz);
-    if (p.c.d == 64) {
-      if (p.bf16) relation_kernel<64, __nv_bfloat16><<<grid, 128, 0, s>>>(p);
-      else relation_kernel<64, __half><<<grid, 128, 0, s>>>(p);
-    } else {
-      if (p.bf16) relation_kernel<128, __nv_bfloat16><<<grid, 128, 0, s>>>(p);
-      else relation_kernel<128, __half><<<grid, 128, 0, s>>>(p);
-    }
+    const bool buckets = p.map.kind != RELPOS_MAP_TRUNCATED && p.map.kind != RELPOS_MAP_IDENTITY;
+    void (*f)(TreeParams) =
+        p.c.d == 64
+            ? (p.bf16 ? (buckets ? relation_kernel<64, __nv_bfloat16, true> : relation_kernel<64, __nv_bfloat16, false>)
+                      : (buckets ? relation_kernel<64, __half, true> : relation_kernel<64, __half, false>))
+            : (p.bf16 ? (buckets ? relation_kernel<128, __nv_bfloat16, true> : relation_kernel<128, __nv_bfloat16, false>)
+                      : (buckets ? relation_kernel<128, __half, true> : relation_kernel<128, __half, false>));
+    f<<<grid, 128, 0, s>>>(p);
   }
   note_launch(1);
   return cudaGetLastError();
