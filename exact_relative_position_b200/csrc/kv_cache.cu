@@ -167,22 +167,19 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
   __syncthreads();
   const int cpr = p.c.d / 16;          // pieces of 16 elements to a row
   const int per_tok = 2 * p.c.Hkv * cpr;
-  const int shift = __ffs(cpr) - 1;
+  const int shift = __ffs(cpr) - 1, tshift = __ffs(toks) - 1;   // toks is a power of two
   const bool pow2 = (cpr & (cpr - 1)) == 0;
   const int Hkv = p.c.Hkv, d = p.c.d;
-  int ti = threadIdx.x / per_tok, r = threadIdx.x - ti * per_tok;
+  // the block's tokens of one head after another: their rows follow each other in the cache
+  const int group = toks * cpr;
 #pragma unroll 4
-  for (; ti < toks; r += 256) {
-    while (r >= per_tok) {             // on to the next token, without a division
-      r -= per_tok;
-      ++ti;
-    }
-    if (ti >= toks) break;
+  for (int i = threadIdx.x; i < toks * per_tok; i += 256) {
+    const int kvh = pow2 ? i >> (shift + tshift) : i / group, rem = i - kvh * group;
+    const int ti = pow2 ? rem >> shift : rem / cpr, ch = rem - ti * cpr;
     const long long at = base[ti];
     if (at == -2) continue;
-    const bool is_v = r >= Hkv * cpr;
-    const int rr = is_v ? r - Hkv * cpr : r;
-    const int h = pow2 ? rr >> shift : rr / cpr, ch = rr - h * cpr;
+    const bool is_v = kvh >= Hkv;
+    const int h = is_v ? kvh - Hkv : kvh;
     uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
     if (at >= 0) {
       const long long row = at + ((long long)h << p.c.page_shift);
