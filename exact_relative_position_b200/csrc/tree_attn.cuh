@@ -19,7 +19,9 @@
 // rows as the 8 columns, S^T = K Q^T and O^T = V^T P^T, so that decoding with
 // up to eight query heads to a key head fills the tile.  With so few rows each
 // loaded element feeds few multiply-adds and the kernel is bound by memory;
-// 128-row tcgen05 tiles would run mostly empty.
+// 128-row tcgen05 tiles would run mostly empty.  64 single tokens over up to 8192
+// keys, 32 / 8 heads of 128: e4m3 129 us (5.5 TB/s, 84% of a plain copy's rate); half
+// of them over bf16 116 us (91% of it).  More rows over a 16-bit cache: tree_wide.cu.
 //
 // Order of the operands.  An MMA sums over k in any order and names its rows in
 // any order, as long as both operands agree.  Each lane of a quad therefore
@@ -1068,7 +1070,11 @@ cudaError_t run_tiling(const TreeParams& p, cudaStream_t s) {
 // Tilings by head dimension and row count.  Up to 32 rows (16 at d = 128, where
 // the outputs take twice the registers) four warps take different keys; beyond
 // that warps share keys and take different rows.  Stages are sized for BPS blocks
-// to an SM with some 100 KB of loads in flight.
+// to an SM with some 100 KB of loads in flight.  A step of 32 keys in place of 16
+// halves the votes and loop code of a step: int8, d = 64, 16 rows 41.7 to 35.1 us (at three
+// blocks to an SM in place of four, for the registers), 32 rows 72 to 66; int8, d = 128, 8
+// rows 115 to 106; 16-bit caches at d = 128 have no registers for it.  Two warps to 16 rows
+// each beat one with 32 (72 to 66 us: the wider warp spills).
 template <int D, bool WIDE> struct Tilings;
 template <bool WIDE> struct Tilings<64, WIDE> {
   using R8 = Tiling<64, 1, 4, 1, 32, 32, WIDE ? 2 : 3, WIDE ? 3 : 4>;

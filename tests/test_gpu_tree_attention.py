@@ -103,6 +103,13 @@ def test_identity_table_longer_than_the_cache():
     check_tree(call(s, max_seqlen=None), want(s), F16)
 
 
+@pytest.mark.parametrize("T,H,dt", [(3, 4, BF16), (40, 8, F16)])            # 6 rows; 160, the many-row kernel
+def test_identity_over_a_long_cache(T, H, dt):
+    # more offsets than any bucketed map has, over several blocks of the projection
+    s = make(B=2, H=H, Hkv=2, T=T, lens=[3001, 1290], page=16, dt=dt, map=rp.RelPosMap("identity"), aq="head", b=True, tree="tree")
+    check_tree(call(s), want(s), dt)
+
+
 def test_positions_past_the_table_are_clamped():
     s = make(B=1, H=2, Hkv=2, T=3, lens=[90], map=rp.RelPosMap("identity"), aq="shared", b=True, N=50)
     check_tree(call(s), want(s), F16)
