@@ -325,7 +325,8 @@ typedef struct {
 
 typedef struct {
   relpos_kv_cache cache;     /* written */
-  int32_t B, N;              /* tokens: k, v are [B, kv_heads, N, d] views (packed: as for relpos_rotary) */
+  int32_t B, N;              /* tokens: k, v are [B, kv_heads, N, d] views (packed: as for relpos_rotary);
+                                B N kv_heads < 2^31 */
   int32_t dtype;             /* RELPOS_F16 or RELPOS_BF16; equal to the format of a 16-bit cache */
   int32_t pad;
   const void *k, *v;         /* device; rows 16-byte aligned (strides multiples of 8 elements) */
@@ -401,7 +402,11 @@ int relpos_tree_workspace_size(const relpos_tree_args* a, size_t* bytes);
  * plain decoding.  With the same inputs the result does not depend on what
  * else runs, and equal calls give equal bits.  workspace: device, 256-byte
  * aligned, contents ignored; calls that may overlap on the GPU need workspaces
- * of their own.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+ * of their own.  Its first word is a status word (relpos_check_workspace): the kernel
+ * that takes more than 64 rows (H / kv_heads x T) over a 16-bit cache bounds its waits as
+ * the layer's do.  Errors: INVALID_ARG (also for more than 2^30 tiles of 64 keys over all
+ * sequences, key heads and row blocks, counted at the page table's width), UNSUPPORTED,
+ * WORKSPACE, CUDA. */
 int relpos_tree_attn(const relpos_tree_args* a, void* workspace, size_t ws_bytes, relpos_stream_t stream);
 
 /* --- measurement ---------------------------------------------------------- */
