@@ -12,6 +12,7 @@ device.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import struct
@@ -132,10 +133,10 @@ class RotaryMap:
         w = self.angular()
         if not all(math.isfinite(x) for x in w):
             raise RelPosError("frequencies must be finite")
-        # turns per position modulo 1, in units of 2^-64 (exact products: the kernel wraps them)
+        # turns per position modulo 1, in units of 2^-64 (exact products: the kernel wraps them).  An
+        # array, whose address is taken at each call: a copy of the map has, and uses, its own.
         steps = [int(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % (1 << 64) for x in w]
-        object.__setattr__(self, "_steps", (ctypes.c_uint64 * (r // 2))(*steps))
-        object.__setattr__(self, "_steps_ptr", ctypes.addressof(self._steps))
+        object.__setattr__(self, "_steps", array.array("Q", steps))
         m = self.magnitude
         if m is None:
             m = 0.1 * math.log(self.factor) + 1.0 if self.scaling == "yarn" and self.factor > 1 else 1.0
@@ -195,7 +196,7 @@ def relpos_rotary(q, k=None, positions=None, *, rotary: RotaryMap, inverse: bool
     else:
         blocks += _NO_TENSOR
     a = _ROTARY.pack(1 if k is None else 2, B, N, d, rotary.rotary_dim, rotary.interleaved, _DTYPES[dt], inverse,
-                     rotary._magnitude, pos_bytes, pos_ptr, pos_bs, rotary._steps_ptr, *blocks)
+                     rotary._magnitude, pos_bytes, pos_ptr, pos_bs, rotary._steps.buffer_info()[0], *blocks)
     _launch("relpos_rotary", dev, a)
     return yq if k is None else (yq, yk)
 
