@@ -285,14 +285,27 @@ class KVCache:
             _cuda(name, t, dt, dev)
             if not t.is_contiguous() or (dt == torch.float32 and t.shape != k.shape[:3]):
                 raise RelPosError(f"{name} must be contiguous" + (" [num_pages, kv_heads, page_size]" if dt == torch.float32 else ""))
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._pages = (k, v, k_scale, v_scale)
         self.num_pages, self.kv_heads, self.page_size, self.d = k.shape
         self.dtype, self.device, self.coded = k.dtype, dev, coded
         if self.page_size < 1 or self.page_size & (self.page_size - 1):
             raise RelPosError("page_size must be a power of two")
-        self._fields = (self.num_pages, self.page_size, self.kv_heads, self.d, CACHE_FORMATS[k.dtype], 0, k.data_ptr(),
-                        v.data_ptr(), k_scale.data_ptr() if coded else 0, v_scale.data_ptr() if coded else 0)
+        self._geometry = (self.num_pages, self.page_size, self.kv_heads, self.d, CACHE_FORMATS[k.dtype], 0)
         self._sizes = {}                                 # workspace bytes by call shape
+
+    # the tensors the pool was made over; another set of tensors is another KVCache
+    k = property(lambda self: self._pages[0])
+    v = property(lambda self: self._pages[1])
+    k_scale = property(lambda self: self._pages[2])
+    v_scale = property(lambda self: self._pages[3])
+
+    def _fields(self):
+        """The argument block's cache: the pointers are the tensors' own at each call, so that a
+        copy of the pool works on its own pages."""
+        k, v, ks, vs = self._pages
+        if ks is None:
+            return (*self._geometry, k.data_ptr(), v.data_ptr(), 0, 0)
+        return (*self._geometry, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
 
 def kv_cache(num_pages: int, page_size: int, kv_heads: int, d: int, dtype: torch.dtype, device="cuda") -> KVCache:
@@ -330,7 +343,7 @@ def kv_cache_write(cache: KVCache, k, v, slots) -> None:
         raise RelPosError("the last dimension of k and v must be contiguous")
     if not slots.is_contiguous():
         slots = slots.contiguous()
-    a = _WRITE.pack(*cache._fields, B, N, _DTYPES[dt], 0, k.data_ptr(), v.data_ptr(), *ks, *_view("v", v)[1],
+    a = _WRITE.pack(*cache._fields(), B, N, _DTYPES[dt], 0, k.data_ptr(), v.data_ptr(), *ks, *_view("v", v)[1],
                     slots.data_ptr())
     _launch("relpos_cache_write", dev, a)
 
@@ -369,7 +382,7 @@ def kv_cache_read(cache: KVCache, page_table, cu_seqlens, *, total_tokens: Optio
     if out is None:
         shape = (total_tokens, cache.kv_heads, cache.d)
         k, v = torch.empty(shape, device=dev, dtype=dtype), torch.empty(shape, device=dev, dtype=dtype)
-    a = _READ.pack(*cache._fields, page_table.shape[0], page_table.shape[1], total_tokens, _DTYPES[dtype],
+    a = _READ.pack(*cache._fields(), page_table.shape[0], page_table.shape[1], total_tokens, _DTYPES[dtype],
                    page_table.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr())
     _launch("relpos_cache_read", dev, a)
     return k, v
@@ -389,7 +402,7 @@ def _workspace_bytes(cache, B, T, H, P, code, aq, b, per_head, desc, N):
     need = cache._sizes.get(key)
     if need is None:
         fake = 256                                       # only a table's not being NULL is read
-        block = _TREE.pack(*cache._fields, B, T, H, 0, code, code, 1.0, N, P, per_head, *desc, 0, *(0,) * 15,
+        block = _TREE.pack(*cache._fields(), B, T, H, 0, code, code, 1.0, N, P, per_head, *desc, 0, *(0,) * 15,
                            fake if aq else 0, fake if b else 0, 0, 0)
         n = ctypes.c_size_t()
         _check(_calls().relpos_tree_workspace_size(block, ctypes.byref(n)), "relpos_tree_workspace_size")
@@ -489,7 +502,7 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise RelPosError(f"workspace must be contiguous on {dev}")
-    a = _TREE.pack(*cache._fields, B, T, H, 0, code, F32 if out_f32 else code, tau, N, P, per_head, *desc, per_seq,
+    a = _TREE.pack(*cache._fields(), B, T, H, 0, code, F32 if out_f32 else code, tau, N, P, per_head, *desc, per_seq,
                    page_table.data_ptr(), lengths.data_ptr(), mask_ptr, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0],
                    qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], 0 if aq is None else aq.data_ptr(),
                    0 if b is None else b.data_ptr(), o.data_ptr(), lse.data_ptr())
