@@ -62,6 +62,13 @@ struct WideShared {
   int warp_sums[kThreads / 32];
 };
 
+// Dynamic shared memory of a block, and the most that one can have beside the static part
+// (and 64 bytes of reserve): the ring of tiles, a kilobyte to align it, the list of sequences.
+// 255 sequences fit at d = 128, thousands at d = 64.
+constexpr int kDynamicMost = 227 * 1024 - (int)sizeof(WideShared) - 64;
+template <int D> constexpr int dynamic_bytes(int B) { return (int)Wide<D>::kOffEnd + 1024 + (((B + 1) * 4 + 127) & ~127); }
+static_assert(dynamic_bytes<128>(1) <= kDynamicMost && dynamic_bytes<64>(4096) <= kDynamicMost, "the tiles of a block do not fit");
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -637,10 +644,9 @@ cudaError_t run_wide(const TreeParams& p, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int most = 227 * 1024 - (int)sizeof(WideShared) - 64;
-  const int smem = (int)Wide<D>::kOffEnd + 1024 + (((p.B + 1) * 4 + 127) & ~127);
+  const int smem = dynamic_bytes<D>(p.B);
   if (dev > 63 || !(ready.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(tree_wide_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    e = cudaFuncSetAttribute(tree_wide_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamicMost);
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready |= 1ull << dev;
   }
@@ -666,13 +672,16 @@ cudaError_t run_wide(const TreeParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Whether this kernel takes a call: more rows than the narrow one's largest block
-// and a cache of the queries' type (the list of sequences has to fit behind the ring
-// of tiles).  16 sequences of up to 8192, 32 / 8 heads, bf16, against the narrow
+// Whether this kernel takes a call: more rows than the narrow one's largest block,
+// a cache of the queries' type, and a list of sequences that fits behind the ring of
+// tiles.  16 sequences of up to 8192, 32 / 8 heads, bf16, against the narrow
 // kernel: d = 128, 244 rows 176 us and 539, 68 rows 131 and 266; d = 64, 68 rows 108 and
 // 162; with one relation row per offset (4 sequences of 4096) 244 rows 197 and 234, 68
 // rows 104 and 117.
-bool takes_wide(const TreeParams& p) { return p.G * p.T > 64 && p.B <= 256; }
+bool takes_wide(const TreeParams& p) {
+  const int smem = p.c.d == 64 ? dynamic_bytes<64>(p.B) : dynamic_bytes<128>(p.B);
+  return p.G * p.T > 64 && smem <= kDynamicMost;
+}
 
 cudaError_t launch_wide(const TreeParams& p, cudaStream_t s) {
   if (p.c.d == 64) return p.bf16 ? run_wide<64, __nv_bfloat16>(p, s) : run_wide<64, __half>(p, s);
