@@ -151,6 +151,7 @@ thread_local int g_last_cuda_error = 0;
 
 int cuda_fail(cudaError_t e) {
   g_last_cuda_error = (int)e;
+  cudaGetLastError();   // the runtime keeps it otherwise, and the next launch would report it
   return RELPOS_ERR_CUDA;
 }
 
