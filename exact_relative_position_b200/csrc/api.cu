@@ -866,9 +866,10 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
     p->R = rows_of(a->map, a->max_seqlen);
     int lo, hi;
     map_bounds(a->map, a->max_seqlen, &lo, &hi);
-    // the reachable part of the expanded range: cached keys lie up to cap + T behind
-    // a node, nodes up to T ahead
-    const int back = -(int)(cap + a->T), ahead = a->T;
+    // the reachable part of the expanded range: a node at depth T - 1 looks cap + T - 1 back at
+    // the first cached key, nodes lie less than T ahead.  However long the table is, the row of
+    // offsets is no longer than for one that just covers the pages and the nodes.
+    const int back = -(int)(cap + a->T - 1), ahead = a->T;
     if (lo > ahead) hi = lo;
     else if (hi < back) lo = hi;
     else { lo = std::max(lo, back); hi = std::min(hi, ahead); }

@@ -18,3 +18,11 @@ def test_batches_around_the_list_of_sequences_of_a_block(B, d, dt):
     check_tree(call(s), want(s), dt)
     y = rp.relpos_rotary(s["q"], rotary=rp.RotaryMap(d, magnitude=0.0))      # what follows is not disturbed
     assert bool((y == 0).all())
+
+
+@pytest.mark.parametrize("T,n", [(4, 64), (7, 30), (40, 57)])
+def test_a_workspace_by_the_helper_serves_a_longer_identity_table(T, n):
+    s = make(B=1, H=4, Hkv=2, T=T, lens=[n], page=64, map=rp.RelPosMap("identity"), aq="head", b=True, N=500, tree="tree")
+    ws = torch.empty(rp.tree_workspace_size(s["cache"], 1, T, 4, 1, aq=True, b=True, map=s["map"]), dtype=torch.uint8, device="cuda")
+    check_tree(call(s, workspace=ws), want(s), F16)
+    check_tree(call(s, workspace=ws, max_seqlen=None), want(s), F16)
