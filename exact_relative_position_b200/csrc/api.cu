@@ -805,18 +805,36 @@ bool is16(int dtype) { return dtype == RELPOS_F16 || dtype == RELPOS_BF16; }
 bool wide_cache(int format) { return format == RELPOS_CACHE_F16 || format == RELPOS_CACHE_BF16; }
 bool same_type(int format, int dtype) { return (format == RELPOS_CACHE_BF16) == (dtype == RELPOS_BF16); }
 
-// Saturation bounds of a map.  Offsets beyond max_distance share a row, so a
-// bucketed map is scanned over that many at most; the last map's bounds are kept
-// per thread, since a decoder asks for the same ones at every step.
+// The bounds of bounds_of.  Rows of a bucketed map change in one direction with the
+// distance on either side of 0, so each run's end is found by bisection there; it may lie far
+// beyond max_distance (an odd number of log buckets: its last row begins where the logarithm
+// has counted one bucket more).  The last map's bounds are kept per thread, since a decoder
+// asks for the same ones at every step.
 void map_bounds(const relpos_map_desc& m, int N, int* lo, int* hi) {
   if (m.kind == RELPOS_MAP_TRUNCATED || m.kind == RELPOS_MAP_IDENTITY) return bounds_of(m, N, lo, hi);
-  const int n = (int)std::min<long long>(N, (long long)m.max_distance + 2);
-  struct Memo { relpos_map_desc m; int n, lo, hi; };
+  struct Memo { relpos_map_desc m; int N, lo, hi; };
   static thread_local Memo memo = {{-1, 0, 0, 0, 0}, 0, 0, 0};
-  if (memo.n != n || memcmp(&memo.m, &m, sizeof(m)) != 0) {
-    bounds_of(m, n, &memo.lo, &memo.hi);
+  if (memo.N != N || memcmp(&memo.m, &m, sizeof(m)) != 0) {
+    // the furthest offset from `from` in direction dir that still has its row, one side at a time
+    auto run = [&](int from, int dir) {
+      const int row = phi_of(m, N, from);
+      int at = from;
+      for (const int end : {0, -from}) {
+        const int first = end == 0 ? at : dir;           // the far side begins one past 0
+        if (end != 0 && (at != 0 || from == 0 || phi_of(m, N, first) != row)) break;
+        int same = first, other = end + dir;             // rows alike up to `same`, not from `other` on
+        while (abs(other - same) > 1) {
+          const int mid = same + (other - same) / 2;
+          if (phi_of(m, N, mid) == row) same = mid; else other = mid;
+        }
+        at = same;
+      }
+      return at;
+    };
+    memo.lo = run(1 - N, 1);
+    memo.hi = std::max(run(N - 1, -1), memo.lo);
     memo.m = m;
-    memo.n = n;
+    memo.N = N;
   }
   *lo = memo.lo;
   *hi = memo.hi;

@@ -37,3 +37,32 @@ def test_the_helper_covers_longer_identity_tables(lib, pages, page, T):
     helper = _bytes(lib, m, pages * page + T, pages, page, T=T)
     for N in (1, pages * page, pages * page + T + 1, pages * page + 64, 10000):
         assert _bytes(lib, m, N, pages, page, T=T) <= helper
+
+
+MAPS = [rp.RelPosMap("log", num_buckets=5, max_distance=64), rp.RelPosMap("log", num_buckets=16, max_distance=64),
+        rp.RelPosMap("log_rev", num_buckets=5, max_distance=64), rp.RelPosMap("log_rev", num_buckets=33, max_distance=128),
+        rp.RelPosMap("log", num_buckets=2, max_distance=8), rp.RelPosMap("log", num_buckets=3, max_distance=9),
+        rp.RelPosMap("log", num_buckets=256, max_distance=512),
+        rp.RelPosMap("t5", num_buckets=32, max_distance=128, bidirectional=0), rp.RelPosMap("t5", num_buckets=7, max_distance=50, bidirectional=0),
+        rp.RelPosMap("t5", num_buckets=32, max_distance=128, bidirectional=1), rp.RelPosMap("t5", num_buckets=10, max_distance=1000, bidirectional=1),
+        rp.RelPosMap("truncated", clip=0), rp.RelPosMap("truncated", clip=9), rp.RelPosMap("identity")]
+
+
+@pytest.mark.parametrize("m", MAPS, ids=lambda m: f"{m.kind}-{m.num_buckets or m.clip}-{m.max_distance}-{m.bidirectional}")
+def test_relation_rows_end_where_the_map_saturates(lib, m):
+    # the layer's own bounds scan every offset; the stored offsets are those between them that can be reached
+    for T in (1, 5):
+        for pages in (1, 4, 150):                        # capacity 16, 64 and 2400
+            for N in (1, 2, 17, 64 + T, 130, 2400 + T, 5000):
+                lo, hi = ctypes.c_int32(), ctypes.c_int32()
+                assert lib.relpos_expanded_bounds(ctypes.byref(m.desc()), N, ctypes.byref(lo), ctypes.byref(hi)) == 0
+                lo, hi, back = lo.value, hi.value, -(16 * pages + T - 1)
+                if lo > T:
+                    hi = lo
+                elif hi < back:
+                    lo = hi
+                else:
+                    lo, hi = max(lo, back), min(hi, T)
+                columns = (hi - lo + 1 + 7) // 8 * 8
+                rows = _bytes(lib, m, N, pages, 16, T=T) - _bytes(lib, m, N, pages, 16, T=T, aq=None, b=None)
+                assert rows == -(-4 * columns * T * 2 // 256) * 256, (T, pages, N)
