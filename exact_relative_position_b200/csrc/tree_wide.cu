@@ -55,7 +55,7 @@ constexpr int kBarQFull = 0, kBarQFree = 1, kBarSFull = 2, kBarPReady = 4, kBarO
 struct WideShared {
   uint64_t bar[kBars];
   uint32_t valid[kTileRing][4];
-  int odd[4];                           // item number + 1 whose nodes hold non-finite values, by its last two bits
+  int odd[4];                           // number + 1 of the part whose nodes hold non-finite values, by its last two bits
   int depth[2][64];
   int abort;
   uint32_t tmem;
@@ -578,7 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
       const bool whole = s.t0 == 0 && s.t1 == s.nt;
-      const bool odd = s.t1 == s.nt && *static_cast<volatile int*>(&sh.odd[seg_no & 3]) == (int)seg_no + 1;
+      // nodes of this part's tiles, which may hold non-finite values: an item may be cut between its nodes
+      const bool odd = *static_cast<volatile int*>(&sh.odd[seg_no & 3]) == (int)seg_no + 1;
+      const int u0 = max(s.t0 * kKeys - s.len, 0), u1 = min(s.t1 * kKeys - s.len, p.T);
       // a padding node, or a row with no key, gives 0; a part is joined (and divided) later
       const bool empty = mk == 0 || l_run == 0.f;
       const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l_run;
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
         tmem_wait_ld();
         if (odd && row_ok) {
-          for (int u = 0; u < p.T; ++u) {
+          for (int u = u0; u < u1; ++u) {
             if (!((mk >> u) & 1ull)) continue;
             const QT* src = static_cast<const QT*>(p.v) + s.b * p.vs.b + s.hkv * p.vs.h + u * p.vs.n + c;
 #pragma unroll

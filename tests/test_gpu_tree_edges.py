@@ -11,6 +11,28 @@ from test_gpu_tree_attention import BF16, E4M3, F16, INT8, TYPE_IDS, TYPES, call
 from tree_definition import check, definition
 
 pytestmark = pytest.mark.gpu
+SPLIT = [(1, 2, 1, 64, 64, 100), (1, 2, 1, 40, 128, 120), (2, 6, 2, 60, 64, 250)]     # B, H, Hkv, T, d, length
+
+
+@pytest.mark.parametrize("val", [math.nan, math.inf], ids=["nan", "inf"])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("B,H,Hkv,T,d,n", SPLIT)
+def test_a_non_finite_value_of_a_node_reaches_its_rows_across_pieces(val, dt, B, H, Hkv, T, d, n):
+    # the nodes lie in two tiles of keys, and so few tiles are pieces of one tile each
+    s = make(B=B, H=H, Hkv=Hkv, T=T, d=d, lens=[n] * B, dt=dt)
+    # node 0 is attended by its children of odd number only; the others descend from node 1
+    s["mask"] = rp.tree_masks([-1, -1] + [0 if t % 2 else 1 for t in range(2, T)]).cuda()
+    clean = call(s)
+    for node in (0, T - 1):                              # in the first of the two tiles, and in the last
+        bad = {**s, "v": s["v"].clone()}
+        bad["v"][:, :, node, 5] = val
+        o, lse = call(bad)
+        sees = torch.tensor([(int(x) >> node) & 1 for x in s["mask"].tolist()]).bool().cuda()
+        assert torch.equal(lse, clean[1])
+        assert torch.equal(o[:, :, ~sees], clean[0][:, :, ~sees])
+        assert bool((~torch.isfinite(o[:, :, sees, 5])).all())
+        cols = [i for i in range(d) if i != 5]
+        assert torch.equal(o[:, :, sees][..., cols], clean[0][:, :, sees][..., cols])
 
 
 @pytest.mark.parametrize("dt,fmt", [(F16, F16), (BF16, INT8)], ids=["f16", "bf16-int8"])
