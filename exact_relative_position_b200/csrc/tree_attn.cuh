@@ -41,6 +41,11 @@
 // running maximum of that sum, and the softmax sum divides it out in fp32:
 //   P'_ij = 2^(s_ij + log2 sv_j - m_i),  l_i = sum_j P'_ij / sv_j,
 //   O_i = sum_j P'_ij code_j / l_i,      LSE_i = m_i + log2 l_i (base 2).
+// A value row of zeros is stored with scale 1.  Taken at that, a key that is attended
+// strongly and holds zeros (they are common where a model parks its attention) would set
+// m_i far above what the other keys, with scales of 2^-10, add to O, and their 16-bit weights
+// would be subnormal or 0.  Such a row enters at 2^-64: it adds nothing to O at any scale,
+// and its share of l_i, kept in fp32, is exact for the others' scales up to 2^30.
 // bf16 queries enter in fp16 after an exact power-of-two scaling of the
 // warp's rows to a largest element in [2^14, 2^15).
 #pragma once
@@ -214,6 +219,10 @@ __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w) {
 }
 // The power e with |x| 2^-e in [2^14, 2^15) for the largest |x| given by its bits.
 __device__ __forceinline__ int exp_of(uint32_t bits) { return iclamp((int)(bits >> 23) - 127 - 14, -100, 100); }
+
+// What a value row of zeros counts as (see above): as a scale, and as a node's power.
+constexpr float kZeroRowScale = 0x1p-64f;
+constexpr int kZeroRowPower = -64;
 
 // An infinity or NaN of a node's value row must not reach the rows that do not
 // attend the node (0 times it is NaN): such elements enter the MMA as 0 and are
@@ -659,13 +668,38 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       }
       float rsv[SG][2];                                 // 1 / value scale of the thread's keys
       if (!WIDE) {
+        bool unit_scale = false;
+#pragma unroll
+        for (int g = 0; g < SG; ++g)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            rsv[g][j] = __uint_as_float(lds32(sk + 2 * HALF + (KW + ko + 16 * g + key0 + 2 * j) * 4));
+            unit_scale = unit_scale || rsv[g][j] == 1.f;
+          }
+        if (__any_sync(0xffffffffu, unit_scale)) {      // rows of zeros?  A quad looks at its keys' codes
+#pragma unroll
+          for (int g = 0; g < SG; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t any = 0;
+#pragma unroll
+              for (int u = 0; u < CPR / 4; ++u) {
+                const uint4 w = lds128(sv + chunk_at<CPR, WIDE, true>(ko + 16 * g + key0 + 2 * j, 4 * u + q4));
+                any |= w.x | w.y | w.z | w.w;
+              }
+              if (FMT == RELPOS_CACHE_E4M3) any &= 0x7f7f7f7fu;   // -0 is a zero
+              any |= __shfl_xor_sync(0xffffffffu, any, 1);
+              any |= __shfl_xor_sync(0xffffffffu, any, 2);
+              if (any == 0 && rsv[g][j] == 1.f) rsv[g][j] = kZeroRowScale;
+            }
+        }
 #pragma unroll
         for (int g = 0; g < SG; ++g)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t a = sk + 2 * HALF + (ko + 16 * g + key0 + 2 * j) * 4;
             const float kcol = __uint_as_float(lds32(a)) * kc;
-            float v = __uint_as_float(lds32(a + KW * 4));
+            float v = rsv[g][j];
             v = v < 0x1p-100f ? 0x1p-100f : v;          // not fmaxf, which would drop the NaN of a spoilt row
             const float lg = lg2(v);
             rsv[g][j] = rcp(v);
@@ -881,7 +915,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
             }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) vt = max(vt, __shfl_xor_sync(0xffffffffu, vt, o));
-            ve[i] = exp_of(vt);
+            ve[i] = vt == 0 ? kZeroRowPower : exp_of(vt);
             vdown[i] = pow2i(-ve[i]);
           }
         }

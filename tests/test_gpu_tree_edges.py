@@ -11,6 +11,10 @@ from test_gpu_tree_attention import BF16, E4M3, F16, INT8, TYPE_IDS, TYPES, call
 from tree_definition import check, definition
 
 pytestmark = pytest.mark.gpu
+CODED = [(F16, E4M3), (BF16, E4M3), (F16, INT8), (BF16, INT8)]
+CODED_IDS = ["f16-e4m3", "bf16-e4m3", "f16-int8", "bf16-int8"]
+ROWS = [(1, 1, 1, 64), (4, 1, 4, 128), (4, 2, 13, 64), (2, 1, 30, 128), (8, 1, 20, 64)]   # H, Hkv, T, d: 1, 16, 26, 60, 160 rows
+ROW_IDS = ["r1", "r16", "r26", "r60", "r160"]
 SPLIT = [(1, 2, 1, 64, 64, 100), (1, 2, 1, 40, 128, 120), (2, 6, 2, 60, 64, 250)]     # B, H, Hkv, T, d, length
 
 
@@ -33,6 +37,63 @@ def test_a_non_finite_value_of_a_node_reaches_its_rows_across_pieces(val, dt, B,
         assert bool((~torch.isfinite(o[:, :, sees, 5])).all())
         cols = [i for i in range(d) if i != 5]
         assert torch.equal(o[:, :, sees][..., cols], clean[0][:, :, sees][..., cols])
+
+
+def _values_of_one_size(s, size):
+    """All value rows of about `size`, with a mean that does not cancel in a sum."""
+    g = torch.Generator().manual_seed(11)
+    c = s["cache"]
+    rows = lambda *shape: (size * (1 + 0.3 * torch.randn(*shape, generator=g))).to(s["q"].dtype).cuda()
+    n = c.num_pages * c.page_size
+    k = torch.randn(n, c.kv_heads, c.d, generator=g).to(s["q"].dtype).cuda()
+    rp.kv_cache_write(c, k, rows(n, c.kv_heads, c.d), torch.arange(n).cuda())
+    s["v"] = rows(*s["v"].shape)
+
+
+def _dominated(dt, fmt, H, Hkv, T, d, size, above, zero=False, node=True):
+    """8000 keys and one, a node or a cached key, whose score lies about `above` over theirs for each row."""
+    s = make(B=1, H=H, Hkv=Hkv, T=T, d=d, lens=[8000], page=64, dt=dt, fmt=fmt)
+    _values_of_one_size(s, size)
+    one = s["q"][:, :1, :1].float()
+    s["q"] = (one + 0.05 * torch.randn(s["q"].shape, device="cuda")).to(dt)
+    key = (one[:, 0, 0] * above / (s["tau"] * one.square().sum())).to(dt)                     # tau q.key = above
+    if node:
+        s["k"][:, :, 0] = key
+        if zero:
+            s["v"][:, :, 0] = 0
+    else:
+        slot = torch.tensor([int(s["table"][0, 70]) * 64 + 9]).cuda()
+        row = key.expand(1, Hkv, d).contiguous()
+        rp.kv_cache_write(s["cache"], row, row * 0 if zero else (row * 0 + size).to(dt), slot)
+    return s
+
+
+@pytest.mark.parametrize("dt,fmt", CODED, ids=CODED_IDS)
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS, ids=ROW_IDS)
+@pytest.mark.parametrize("size", [0.02, 1e-4])
+def test_small_values_beside_a_dominating_node(dt, fmt, H, Hkv, T, d, size):
+    s = _dominated(dt, fmt, H, Hkv, T, d, size, 9.5)
+    check(call(s), definition(s), dt)
+
+
+@pytest.mark.parametrize("dt,fmt", CODED, ids=CODED_IDS)
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS, ids=ROW_IDS)
+@pytest.mark.parametrize("node", [True, False], ids=["node", "cached"])
+def test_small_values_beside_a_dominating_row_of_zeros(dt, fmt, H, Hkv, T, d, node):
+    s = _dominated(dt, fmt, H, Hkv, T, d, 0.02, 9.5, zero=True, node=node)
+    check(call(s), definition(s), dt)
+
+
+def test_value_rows_of_zeros_only():
+    for dt, fmt in CODED:
+        s = make(B=2, H=2, Hkv=1, T=3, lens=[70, 9], dt=dt, fmt=fmt)
+        c = s["cache"]
+        z = torch.zeros(c.num_pages * c.page_size, 1, 64, dtype=dt, device="cuda")
+        rp.kv_cache_write(c, z + 1, z, torch.arange(z.shape[0]).cuda())
+        s["v"] *= 0
+        o, lse = call(s)
+        check((o, lse), definition(s), dt)
+        assert bool((o == 0).all())
 
 
 @pytest.mark.parametrize("dt,fmt", [(F16, F16), (BF16, INT8)], ids=["f16", "bf16-int8"])

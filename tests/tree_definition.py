@@ -2,10 +2,12 @@
 error bounds that follow from what enters the 16-bit product P V: weights in
 16 bits next to values, or to 8-bit codes whose scales are the values' own.
 
-A weight is off by half a step of its type relative to itself, and in fp16 by
-2^-25 of the largest contribution's unit where it is subnormal.  The unit of an
-8-bit cache's key is its value scale, of a node the power of two that brings its
-row to 2^14 .. 2^15; a value row of zeros contributes nothing and sets no unit."""
+A weight is off by half a step of its type relative to itself, and in fp16, where
+it is subnormal, by 2^-25 of the largest weight so far.  It multiplies the unit of its
+key: over an 8-bit cache the value scale of a cached key (a value row of zeros sets
+none), and of a node 1, or in bf16 the power of two that brings its row to 2^14 ..
+2^15.  Cached keys come before the nodes, so their weights are measured by the
+largest cached one."""
 import math
 
 import torch
@@ -60,18 +62,26 @@ def definition(s, hidden=None):
             E[bi, h] = torch.logsumexp(S, 1)
             tE[bi, h] = 2 * ds + 2.0 ** -22 * E[bi, h].abs().nan_to_num(0, 0, 0)
             P = torch.where(keep.any(1)[:, None], torch.softmax(S, 1), torch.zeros_like(S))
-            top_node = vd[bi, g].abs().nan_to_num(0, 0, 0).amax(-1)
-            unit = torch.cat((vs[g], torch.exp2(torch.floor(torch.log2(top_node)) - 14))) if cache.coded else torch.ones(n + T)
-            live = (V != 0).any(1) & (unit > 0)
-            codes = torch.where(live[:, None], V.abs() / torch.where(live, unit, torch.ones_like(unit))[:, None], torch.zeros_like(V))
+            unit = torch.ones(n + T, dtype=torch.float64)
+            if cache.coded:
+                unit[:n] = vs[g]
+                if q.dtype == torch.bfloat16:
+                    unit[n:] = torch.exp2(torch.floor(torch.log2(vd[bi, g].abs().nan_to_num(0, 0, 0).amax(-1))) - 14)
+            sets = (V != 0).any(1) & (unit > 0)          # keys whose weight may be the largest
+            if cache.coded and q.dtype == torch.float16:
+                sets[n:] = True
+            codes = torch.where(sets[:, None], V.abs() / torch.where(sets, unit, torch.ones_like(unit))[:, None], torch.zeros_like(V))
+            cached = torch.arange(n + T) < n
             for t in range(T):
                 kk = keep[t]
                 if not kk.any():
                     continue
                 O[bi, h, t] = P[t, kk] @ V[kk]
                 tO[bi, h, t] = (P[t, kk] @ V[kk].abs()) * (u16 + 2 * float(ds[t]) + 2.0 ** -20 + int(kk.sum()) * 2.0 ** -23)
-                if fp16 and bool((kk & live).any()):
-                    tO[bi, h, t] += 2.0 ** -25 * (P[t] * unit)[kk & live].max() * codes[kk].sum(0)
+                if fp16:
+                    weight = torch.where(kk & sets, P[t] * unit, torch.zeros_like(unit))
+                    first = weight[:n].max() if n and cache.coded else weight.max()
+                    tO[bi, h, t] += 2.0 ** -25 * (first * codes[kk & cached].sum(0) + weight.max() * codes[kk & ~cached].sum(0))
     return O, E, tO, tE
 
 
