@@ -780,7 +780,11 @@ RELPOS_EXPORT int relpos_debug_tile_plan_device(const relpos_map_desc* map, int3
 namespace {
 
 Strides strides(int64_t b, int64_t h, int64_t n) { return Strides{(long long)b, (long long)h, (long long)n}; }
-bool rows16(const Strides& s) { return s.b % 8 == 0 && s.h % 8 == 0 && s.n % 8 == 0; }
+// Rows of a [B, H, N, ..] view start on 16 bytes where the first does; the stride of a
+// dimension of one means nothing.
+bool rows16(const Strides& s, int B, int H, int N) {
+  return (B <= 1 || s.b % 8 == 0) && (H <= 1 || s.h % 8 == 0) && (N <= 1 || s.n % 8 == 0);
+}
 
 int check_cache(const relpos_kv_cache& c, CacheParams* p) {
   if (c.format < RELPOS_CACHE_F16 || c.format > RELPOS_CACHE_INT8) return RELPOS_ERR_UNSUPPORTED;
@@ -968,7 +972,8 @@ RELPOS_EXPORT int relpos_cache_write(const relpos_cache_write_args* a, relpos_st
   p.k = a->k; p.v = a->v;
   p.kst = strides(a->k_stride_b, a->k_stride_h, a->k_stride_n);
   p.vst = strides(a->v_stride_b, a->v_stride_h, a->v_stride_n);
-  if (!rows16(p.kst) || !rows16(p.vst)) return RELPOS_ERR_INVALID_ARG;
+  const int Hkv = a->cache.kv_heads;
+  if (!rows16(p.kst, a->B, Hkv, a->N) || !rows16(p.vst, a->B, Hkv, a->N)) return RELPOS_ERR_INVALID_ARG;
   if ((long long)a->B * a->N >= (1LL << 31) / a->cache.kv_heads) return RELPOS_ERR_INVALID_ARG;
   p.B = a->B; p.N = a->N;
   p.slots = reinterpret_cast<const long long*>(a->slots);
@@ -1017,7 +1022,9 @@ RELPOS_EXPORT int relpos_tree_attn(const relpos_tree_args* a, void* workspace, s
   const void* al[] = {a->q, a->k, a->v, a->aq, a->o};
   for (const void* x : al)
     if (x && !aligned16(x)) return RELPOS_ERR_INVALID_ARG;
-  if (!rows16(p.qs) || !rows16(p.ks) || !rows16(p.vs)) return RELPOS_ERR_INVALID_ARG;
+  const int Hkv = a->cache.kv_heads;
+  if (!rows16(p.qs, a->B, a->H, a->T) || !rows16(p.ks, a->B, Hkv, a->T) || !rows16(p.vs, a->B, Hkv, a->T))
+    return RELPOS_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(a->tree_mask) & 7) return RELPOS_ERR_INVALID_ARG;
   if (!workspace || ws_bytes < L.end || (reinterpret_cast<uintptr_t>(workspace) & 255)) return RELPOS_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

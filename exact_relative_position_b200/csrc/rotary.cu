@@ -127,10 +127,12 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
   }
 }
 
-bool fits(const RotaryTensor& t, int V, int es) {
+// Whether all rows start on whole vectors (the stride of a dimension of one means nothing).
+bool fits(const RotaryParams& p, const RotaryTensor& t, int V, int es) {
   const long long m = V;
   auto ok = [&](const void* q, const Strides& s) {
-    return reinterpret_cast<uintptr_t>(q) % (V * es) == 0 && s.b % m == 0 && s.h % m == 0 && s.n % m == 0;
+    return reinterpret_cast<uintptr_t>(q) % (V * es) == 0 && (p.B == 1 || s.b % m == 0) && (t.H == 1 || s.h % m == 0) &&
+           (p.N == 1 || s.n % m == 0);
   };
   return ok(t.x, t.xs) && ok(t.y, t.ys);
 }
@@ -156,7 +158,7 @@ cudaError_t go(const RotaryParams& p, cudaStream_t s) {
 template <typename T, int V>
 cudaError_t pick(const RotaryParams& p, cudaStream_t s) {
   bool wide = p.rotary_dim % (2 * V) == 0 && p.d % V == 0;
-  for (int i = 0; i < p.n_tensors; ++i) wide = wide && fits(p.t[i], V, sizeof(T));
+  for (int i = 0; i < p.n_tensors; ++i) wide = wide && fits(p, p.t[i], V, sizeof(T));
   return wide ? go<T, V>(p, s) : go<T, 1>(p, s);
 }
 

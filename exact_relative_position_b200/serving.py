@@ -220,7 +220,7 @@ def _rotary_tensor(x, H, st, y):
             raise RelPosError("out must have its input's shape and a contiguous last dimension")
         if 0 in (s for s, n in zip(y.stride(), y.shape) if n > 1):
             raise RelPosError("out must not be an expanded tensor")
-        if y.data_ptr() == x.data_ptr() and y.stride() != x.stride():
+        if y.data_ptr() == x.data_ptr() and any(a != b for a, b, n in zip(y.stride(), x.stride(), x.shape) if n > 1):
             raise RelPosError("an output in place must have its input's strides")
     yst = st if y.stride() == x.stride() else _view("out", y)[1]
     return y, (x.data_ptr(), y.data_ptr(), H, 0, *st, *yst), x

@@ -329,7 +329,7 @@ typedef struct {
                                 B N kv_heads < 2^31 */
   int32_t dtype;             /* RELPOS_F16 or RELPOS_BF16; equal to the format of a 16-bit cache */
   int32_t pad;
-  const void *k, *v;         /* device; rows 16-byte aligned (strides multiples of 8 elements) */
+  const void *k, *v;         /* device; rows 16-byte aligned (strides multiples of 8 elements where the dimension is over 1) */
   int64_t k_stride_b, k_stride_h, k_stride_n;
   int64_t v_stride_b, v_stride_h, v_stride_n;
   const int64_t* slots;      /* device [B, N]: page x page_size + offset of each token.  A negative
@@ -381,7 +381,7 @@ typedef struct {
                                 T on are ignored.  NULL: a chain, node i attends nodes 0 .. i */
   const void *q;             /* device [B, H, T, d] view */
   const void *k, *v;         /* device [B, kv_heads, T, d] views: the nodes' own rows, not yet in the cache */
-  int64_t q_stride_b, q_stride_h, q_stride_n;   /* multiples of 8 elements, rows 16-byte aligned */
+  int64_t q_stride_b, q_stride_h, q_stride_n;   /* as for relpos_cache_write_args */
   int64_t k_stride_b, k_stride_h, k_stride_n;
   int64_t v_stride_b, v_stride_h, v_stride_n;
   const void* aq;            /* device table, or NULL */

@@ -105,3 +105,31 @@ def test_an_odd_number_of_buckets(dt, fmt, m, H, Hkv, T):
     s = make(B=2, H=H, Hkv=Hkv, T=T, lens=[2500, 400], page=64, dt=dt, fmt=fmt, map=m, aq="head", b=True)
     s["b"] *= 4
     check(call(s), definition(s), dt)
+
+
+@pytest.mark.parametrize("dt,fmt", [(F16, F16), (BF16, INT8)], ids=["f16", "bf16-int8"])
+def test_strides_of_dimensions_of_one_mean_nothing(dt, fmt):
+    s = make(B=1, H=2, Hkv=1, T=1, d=64, lens=[40], dt=dt, fmt=fmt)
+    want = call(s)
+    z = dict(s)
+    z["q"] = s["q"].as_strided((1, 2, 1, 64), (13, 64, 7, 1))
+    z["k"], z["v"] = (s[x].as_strided((1, 1, 1, 64), (3, 5, 7, 1)) for x in "kv")
+    got = call(z)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_cache_rows_and_rotary_with_strides_of_dimensions_of_one():
+    x = torch.randn(1, 1, 1, 64, device="cuda").half()
+    odd = x.as_strided((1, 1, 1, 64), (3, 5, 7, 1))
+    a, b = (rp.kv_cache(1, 8, 1, 64, INT8) for _ in range(2))
+    at = torch.tensor([[5]]).cuda()
+    rp.kv_cache_write(a, x, x, at)
+    rp.kv_cache_write(b, odd, odd, at)
+    assert torch.equal(a.k, b.k) and torch.equal(a.v_scale, b.v_scale) and bool((a.k[0, 0, 5] != 0).any())
+    rot = rp.RotaryMap(64)
+    pos = torch.tensor([7]).cuda()
+    want = rp.relpos_rotary(x, None, pos, rotary=rot)
+    assert torch.equal(rp.relpos_rotary(odd, None, pos, rotary=rot), want)
+    y = x.clone()                                        # in place through another view of the same rows
+    rp.relpos_rotary(y, None, pos, rotary=rot, out=(y.as_strided((1, 1, 1, 64), (3, 5, 7, 1)),))
+    assert torch.equal(y, want)
