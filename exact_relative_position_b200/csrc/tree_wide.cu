@@ -550,7 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
             m_run = m_new;
           }
         }
-        const float sub = m_run == -INFINITY ? 0.f : rowc - m_run;
+        // with nothing seen yet every score is -inf, if not by its mask then by rowc (a saturated bias
+        // of -inf), which then has to stay in the exponent: 2^(x c2) alone could be infinite
+        const float sub = m_run == -INFINITY ? rowc : rowc - m_run;
         const float2 cc = make_float2(c2, c2), ss = make_float2(sub, sub);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

@@ -107,6 +107,30 @@ def test_an_odd_number_of_buckets(dt, fmt, m, H, Hkv, T):
     check(call(s), definition(s), dt)
 
 
+@pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS, ids=ROW_IDS)
+@pytest.mark.parametrize("tau", [None, 1.0])
+def test_a_bias_of_minus_infinity_hides_far_keys(dt, fmt, H, Hkv, T, d, tau, low=-math.inf):
+    # a window of 20: the saturated row of a truncated map hides all before it
+    s = make(B=2, H=H, Hkv=Hkv, T=T, d=d, lens=[700, 15], dt=dt, fmt=fmt, map=rp.RelPosMap("truncated", clip=20), b=True, tree="tree")
+    s["b"][:, 0] = low
+    if tau is not None:
+        s["tau"] = tau
+    s["q"] *= 3
+    for aq in (None, (0.5 * torch.randn(41, d, device="cuda")).to(dt)):
+        s["aq"] = aq
+        check(call(s), definition(s), dt)
+
+
+def test_a_bias_that_hides_everything():
+    for dt, fmt in TYPES:
+        for H, T in ((2, 3), (4, 30)):
+            s = make(B=1, H=H, Hkv=1, T=T, lens=[300], dt=dt, fmt=fmt, map=rp.RelPosMap("truncated", clip=2), b=True)
+            s["b"][:] = -math.inf
+            o, lse = call(s)
+            assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
 @pytest.mark.parametrize("dt,fmt", [(F16, F16), (BF16, INT8)], ids=["f16", "bf16-int8"])
 def test_strides_of_dimensions_of_one_mean_nothing(dt, fmt):
     s = make(B=1, H=2, Hkv=1, T=1, d=64, lens=[40], dt=dt, fmt=fmt)
