@@ -900,6 +900,7 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
     p->aq = a->aq; p->bias = a->b;
     p->aq_hs = a->table_per_head ? (long long)p->R * a->cache.d : 0;
     p->z_scale = wide_cache(a->cache.format) ? 1.f : p->c2;
+    p->z_limit = 0x1p26f / p->c2;
     p->z_h = a->aq ? zw * a->T : zw;
     p->z_t = a->aq ? zw : 0;
     p->z_b = a->aq ? zw * a->T * a->H : 0;

@@ -82,6 +82,7 @@ struct TreeParams {
   long long z_b, z_h, z_t;            // element strides of z (0 where shared)
   int e_lo, e_hi;
   float z_scale;                      // what z is multiplied by when it is written
+  float z_limit;                      // bound of a finite term before that
   const void* aq;                     // [R, d] or [H, R, d], or null
   long long aq_hs;
   const float* bias;                  // [H, R] or null

@@ -6,6 +6,15 @@ namespace relpos {
 namespace tree {
 namespace {
 
+// A finite term is bounded to 2^26 in base-2 units (e^-4.6e7, where a weight is 0 next to any
+// other): a table may hide keys with the lowest number of its type, and the exponents of a
+// tile that is hidden altogether are s c2 - m with m = s c2 rounded, which is off by half a
+// unit of m's last place: 4 at 2^26, infinite weights further out.  An infinite term stays.
+__device__ __forceinline__ float term(const TreeParams& p, float x) {
+  if (fabsf(x) <= 3.4028235e38f) x = fminf(fmaxf(x, -p.z_limit), p.z_limit);
+  return x * p.z_scale;
+}
+
 // z[b, h, t, e] = z_scale (q . aQ[phi(e_lo + e)] + b[phi(e_lo + e)]): one MMA
 // product of a head's B T query rows with the table rows of the reachable
 // offsets.  A warp keeps 16 table rows in registers and walks over the rows
@@ -81,8 +90,7 @@ __global__ void __launch_bounds__(128) relation_kernel(const __grid_constant__ T
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         if (c0 + 8 * j + 2 * q4 < W)   // rows are padded to whole column tiles
-          *reinterpret_cast<float2*>(dst + 8 * j) = make_float2((acc[j][2 * e] + bias[j][0]) * p.z_scale,
-                                                                (acc[j][2 * e + 1] + bias[j][1]) * p.z_scale);
+          *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(term(p, acc[j][2 * e] + bias[j][0]), term(p, acc[j][2 * e + 1] + bias[j][1]));
     }
   }
 }
@@ -93,7 +101,7 @@ __global__ void __launch_bounds__(128) bias_kernel(const __grid_constant__ TreeP
   const int e = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;
   if (e > p.e_hi - p.e_lo) return;
   const int r = iclamp(phi_of(p.map, p.N, p.e_lo + e), 0, p.R - 1);
-  p.z[h * p.z_h + e] = p.bias[(long long)h * p.R + r] * p.z_scale;
+  p.z[h * p.z_h + e] = term(p, p.bias[(long long)h * p.R + r]);
 }
 
 // Joins the partial results of an item that was cut: pieces c0 .. c1 of the

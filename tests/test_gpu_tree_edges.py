@@ -122,6 +122,13 @@ def test_a_bias_of_minus_infinity_hides_far_keys(dt, fmt, H, Hkv, T, d, tau, low
         check(call(s), definition(s), dt)
 
 
+@pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS, ids=ROW_IDS)
+@pytest.mark.parametrize("tau", [None, 1.0])
+def test_the_lowest_bias_hides_far_keys(dt, fmt, H, Hkv, T, d, tau):
+    test_a_bias_of_minus_infinity_hides_far_keys(dt, fmt, H, Hkv, T, d, tau, low=torch.finfo(torch.float32).min)
+
+
 def test_a_bias_that_hides_everything():
     for dt, fmt in TYPES:
         for H, T in ((2, 3), (4, 30)):
@@ -157,3 +164,12 @@ def test_cache_rows_and_rotary_with_strides_of_dimensions_of_one():
     y = x.clone()                                        # in place through another view of the same rows
     rp.relpos_rotary(y, None, pos, rotary=rot, out=(y.as_strided((1, 1, 1, 64), (3, 5, 7, 1)),))
     assert torch.equal(y, want)
+
+
+def test_the_lowest_bias_everywhere_stays_finite():
+    for dt, fmt in TYPES:
+        for H, T in ((2, 3), (4, 30)):
+            s = make(B=2, H=H, Hkv=1, T=T, lens=[300, 0], dt=dt, fmt=fmt, map=rp.RelPosMap("truncated", clip=2), b=True)
+            s["b"][:] = torch.finfo(torch.float32).min
+            o, lse = call(s)
+            assert bool(torch.isfinite(o).all()) and bool((lse < -1e7).all()) and bool(torch.isfinite(lse).all())
