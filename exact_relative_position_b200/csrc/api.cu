@@ -860,7 +860,7 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
   if (wide_cache(a->cache.format) && !same_type(a->cache.format, a->dtype)) return RELPOS_ERR_UNSUPPORTED;
   if (a->B < 1 || a->B > 4096 || a->T < 1 || a->T > 64 || a->H < 1 || a->H > 65535) return RELPOS_ERR_INVALID_ARG;
   if (a->H % a->cache.kv_heads || a->pages_per_seq < 1) return RELPOS_ERR_INVALID_ARG;
-  if (!(a->tau > 0.f) || a->tau > 3.0e38f) return RELPOS_ERR_INVALID_ARG;
+  if (!(a->tau > 0.f) || a->tau > 2.0e38f) return RELPOS_ERR_INVALID_ARG;   // tau log2 e is finite
   const long long cap = (long long)a->pages_per_seq * a->cache.page_size;
   if (cap > (1LL << 30)) return RELPOS_ERR_INVALID_ARG;
   p->B = a->B; p->T = a->T; p->H = a->H; p->G = a->H / a->cache.kv_heads;

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       lrow[n][0] = lrow[n][1] = 0.f;
     }
     const float unit = WIDE ? p.c2 : 1.f;               // base-2 units of scores and maxima
-    const float slack = WIDE ? 8.f / p.c2 : 8.f;
+    const float slack = WIDE ? fminf(8.f / p.c2, 3e38f) : 8.f;   // (finite for the smallest tau, too)
 
     // moves the maxima where a score exceeds its row's by more than the slack
     auto new_max = [&](const float (&lm)[NR][2]) {

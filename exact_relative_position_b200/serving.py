@@ -445,6 +445,8 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     Hkv = cache.kv_heads
     if d != cache.d or d not in (64, 128) or H % Hkv:
         raise RelPosError("q must have the cache's head dimension (64 or 128) and a multiple of its heads")
+    if not 0 < tau <= 2e38:
+        raise RelPosError("tau must be positive, at most 2e38")
     if not 1 <= T <= MAX_NODES:
         raise RelPosError(f"1 to {MAX_NODES} drafted tokens")
     if k.shape != (B, Hkv, T, d) or v.shape != k.shape:

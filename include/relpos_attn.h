@@ -367,7 +367,7 @@ typedef struct {
                                 kv_heads (query head h reads key head h / (H / kv_heads)); B <= 4096 */
   int32_t dtype;             /* RELPOS_F16 or RELPOS_BF16: q, k, v, aq */
   int32_t out_dtype;         /* dtype, or RELPOS_F32 */
-  float tau;                 /* finite and > 0 */
+  float tau;                 /* > 0, at most 2e38 */
   int32_t max_seqlen;        /* N of the map (its table rows; offsets are clamped to [1 - N, N - 1]) */
   int32_t pages_per_seq;     /* page_table is device int32 [B, pages_per_seq]; a token whose page lies
                                 outside the pool is masked */

@@ -138,6 +138,17 @@ def test_a_bias_that_hides_everything():
             assert bool((o == 0).all()) and bool((lse == -math.inf).all())
 
 
+@pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("T", [1, 33])
+@pytest.mark.parametrize("tau", [1e-39, 1e-30, 1e6])
+def test_tau_far_from_its_usual_size(dt, fmt, T, tau):
+    s = make(B=1, H=2, Hkv=1, T=T, d=64, lens=[200], dt=dt, fmt=fmt)
+    s["tau"] = tau
+    if tau > 1:
+        s["q"] *= 1e-4
+    check(call(s), definition(s), dt)
+
+
 @pytest.mark.parametrize("dt,fmt", [(F16, F16), (BF16, INT8)], ids=["f16", "bf16-int8"])
 def test_strides_of_dimensions_of_one_mean_nothing(dt, fmt):
     s = make(B=1, H=2, Hkv=1, T=1, d=64, lens=[40], dt=dt, fmt=fmt)
@@ -173,3 +184,11 @@ def test_the_lowest_bias_everywhere_stays_finite():
             s["b"][:] = torch.finfo(torch.float32).min
             o, lse = call(s)
             assert bool(torch.isfinite(o).all()) and bool((lse < -1e7).all()) and bool(torch.isfinite(lse).all())
+
+
+def test_a_tau_whose_base_2_form_is_infinite_is_refused():
+    s = make(B=1, H=2, Hkv=1, T=2, lens=[20])
+    for bad in (2.5e38, 1e39, math.inf):
+        s["tau"] = bad
+        with pytest.raises(rp.RelPosError):
+            call(s)
