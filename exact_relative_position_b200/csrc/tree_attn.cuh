@@ -46,8 +46,9 @@
 // m_i far above what the other keys, with scales of 2^-10, add to O, and their 16-bit weights
 // would be subnormal or 0.  Such a row enters at 2^-64: it adds nothing to O at any scale,
 // and its share of l_i, kept in fp32, is exact for the others' scales up to 2^30.
-// bf16 queries enter in fp16 after an exact power-of-two scaling of the
-// warp's rows to a largest element in [2^14, 2^15).
+// bf16 queries enter in fp16 after an exact power-of-two scaling of each row to a
+// largest element in [2^14, 2^15): a power of the row's own, since what a padding node or
+// another head holds must not cost this one its precision.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -495,12 +496,14 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 
     // ---- queries: B fragments in the permuted k order, row r8 of each tile
     uint32_t qb[NR][KS][2];
-    uint32_t top = 0;
+    constexpr bool POWERS = !WIDE && DT<QT>::kCoarse;   // rows of queries have powers of two
+    float kc[NR][2];                                    // scores of 8-bit keys: acc * scale_j * kc (base 2), rows 2 q + e
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       const int r = rb * ROWS + (wm * NR + n) * 8 + r8;
       const int t = r < R ? r / p.G : 0, h = hkv * p.G + (r < R ? r - t * p.G : 0);
       const uint16_t* src = static_cast<const uint16_t*>(p.q) + b * p.qs.b + h * p.qs.h + (long long)t * p.qs.n;
+      uint32_t top = 0;
 #pragma unroll
       for (int u = 0; u < D / 32; ++u) {
         // 16-bit keys: 8 elements at 32 u + 8 q; 8-bit keys: 8 of the 16 elements at 64 (u / 2) + 16 q
@@ -511,24 +514,22 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         qb[n][2 * u][1] = w.y;
         qb[n][2 * u + 1][0] = w.z;
         qb[n][2 * u + 1][1] = w.w;
-        if (!WIDE && DT<QT>::kCoarse) top = amax2(amax2(amax2(amax2(top, w.x), w.y), w.z), w.w);
+        if (POWERS) top = amax2(amax2(amax2(amax2(top, w.x), w.y), w.z), w.w);
       }
-    }
-    float qf = 1.f;                                     // the queries' power of two (8-bit caches)
-    if (!WIDE && DT<QT>::kCoarse) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = exp_of(top);
-      qf = pow2i(e);
-      const float down = pow2i(-e);
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
+      kc[n][0] = kc[n][1] = p.c2;
+      if (POWERS) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int power = exp_of(top);                  // of row r8
+        const float down = pow2i(-power);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int i = 0; i < 2; ++i) qb[n][ks][i] = to_half2<QT>(qb[n][ks][i], down);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) kc[n][e] *= pow2i(__shfl_sync(0xffffffffu, power, 4 * (2 * q4 + e)));
+      }
     }
-    const float kc = p.c2 * qf;                         // scores of 8-bit keys: acc * scale_j * kc (base 2)
 
     // ---- rows 2 q and 2 q + 1 of each tile: their saturated relation terms
     __syncthreads();
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t a = sk + 2 * HALF + (ko + 16 * g + key0 + 2 * j) * 4;
-            const float kcol = __uint_as_float(lds32(a)) * kc;
+            const float ks = __uint_as_float(lds32(a));
             float v = rsv[g][j];
             v = v < 0x1p-100f ? 0x1p-100f : v;          // not fmaxf, which would drop the NaN of a spoilt row
             const float lg = lg2(v);
@@ -708,8 +709,8 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float& x = s[n][g][2 * j + e];
-                if (EASY) x = fmaf(x, kcol, lg + zlow[n][e]);
-                else x = fmaf(x, kcol, p.z ? lg + z.v[n][g][2 * j + e] : lg);
+                if (EASY) x = fmaf(x, ks * kc[n][e], lg + zlow[n][e]);
+                else x = fmaf(x, ks * kc[n][e], p.z ? lg + z.v[n][g][2 * j + e] : lg);
               }
           }
       }
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         auto part = [&](const uint16_t* base, long long stride, int u, int d0) {
           return u < p.T ? __ldg(reinterpret_cast<const uint4*>(base + u * stride + d0)) : make_uint4(0, 0, 0, 0);
         };
-        float down[2] = {1.f, 1.f}, kcol[2] = {kc, kc};
+        float down[2] = {1.f, 1.f}, ks[2] = {1.f, 1.f};
         if (DT<QT>::kCoarse) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -884,7 +885,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
             kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, 2));
             const int e = exp_of(kt);
             down[j] = pow2i(-e);
-            kcol[j] = pow2i(e) * kc;
+            ks[j] = pow2i(e);
           }
         }
 #pragma unroll
@@ -940,7 +941,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
               if (p.z) x += row_z[r][iclamp(du - row_depth[r], p.e_lo, p.e_hi) - p.e_lo];
               const bool keep = u < p.T && ((mk >> (u & 63)) & 1ull);
               float& y = s[n][2 * j + e];
-              y = keep ? fmaf(y, kcol[j], x) : -INFINITY;
+              y = keep ? fmaf(y, ks[j] * kc[n][e], x) : -INFINITY;
               lm[n][e] = fmaxf(lm[n][e], y);
             }
         }

@@ -139,6 +139,21 @@ def test_a_bias_that_hides_everything():
 
 
 @pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS, ids=ROW_IDS)
+def test_a_row_depends_on_its_own_query(dt, fmt, H, Hkv, T, d):
+    # whatever one row holds (a padding node's anything, a head of another size), the others stay within their bounds
+    s = make(B=2, H=H, Hkv=Hkv, T=T, d=d, lens=[90, 40], dt=dt, fmt=fmt, map=rp.RelPosMap("truncated", clip=8), aq="head", b=True)
+    for big in ((3e38, 1e-30) if dt == BF16 else (6e4, 1e-6)):
+        z = {**s, "q": s["q"].clone()}
+        z["q"][0, H - 1, T - 1] = big
+        got, want = call(z), definition(z)
+        rest = [x.flatten(1, 2)[0, :H * T - 1] for x in want]
+        if H * T > 1:
+            check([x.flatten(1, 2)[0, :H * T - 1] for x in got], rest, dt, "the same sequence")
+        check([x[1] for x in got], [x[1] for x in want], dt, "another sequence")
+
+
+@pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
 @pytest.mark.parametrize("T", [1, 33])
 @pytest.mark.parametrize("tau", [1e-39, 1e-30, 1e6])
 def test_tau_far_from_its_usual_size(dt, fmt, T, tau):
