@@ -218,8 +218,10 @@ __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w) {
   m = lo < 0x7f800000u ? max(m, lo) : m;
   return hi < 0x7f800000u ? max(m, hi) : m;
 }
-// The power e with |x| 2^-e in [2^14, 2^15) for the largest |x| given by its bits.
-__device__ __forceinline__ int exp_of(uint32_t bits) { return iclamp((int)(bits >> 23) - 127 - 14, -100, 100); }
+// The power e with |x| 2^-e in [2^14, 2^15) for the largest |x| given by its bits, not below
+// `least`.  Keys and queries go down to -126 (bf16's smallest normal numbers), value rows to -100:
+// they are divided out of the row sum again, which holds 2^-e times a weight.
+__device__ __forceinline__ int exp_of(uint32_t bits, int least) { return max((int)(bits >> 23) - 127 - 14, least); }
 
 // What a value row of zeros counts as (see above): as a scale, and as a node's power.
 constexpr float kZeroRowScale = 0x1p-64f;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       if (POWERS) {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int power = exp_of(top);                  // of row r8
+        const int power = exp_of(top, -126);            // of row r8
         const float down = pow2i(-power);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
@@ -883,7 +885,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
             }
             kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, 1));
             kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, 2));
-            const int e = exp_of(kt);
+            const int e = exp_of(kt, -126);
             down[j] = pow2i(-e);
             ks[j] = pow2i(e);
           }
@@ -916,7 +918,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
             }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) vt = max(vt, __shfl_xor_sync(0xffffffffu, vt, o));
-            ve[i] = vt == 0 ? kZeroRowPower : exp_of(vt);
+            ve[i] = vt == 0 ? kZeroRowPower : exp_of(vt, -100);
             vdown[i] = pow2i(-ve[i]);
           }
         }

@@ -153,6 +153,17 @@ def test_a_row_depends_on_its_own_query(dt, fmt, H, Hkv, T, d):
         check([x[1] for x in got], [x[1] for x in want], dt, "another sequence")
 
 
+@pytest.mark.parametrize("fmt", [E4M3, INT8], ids=["e4m3", "int8"])
+@pytest.mark.parametrize("q,k,v", [(1e-36, 1e36, 1.0), (1e30, 1e-30, 1e37), (1e-30, 3e29, 5e37)])
+def test_bf16_numbers_near_the_ends_of_their_range(fmt, q, k, v):
+    # the nodes alone: an 8-bit cache's own rows are coded with scales of their own
+    s = make(B=1, H=2, Hkv=1, T=9, d=64, lens=[0], dt=BF16, fmt=fmt, tree="tree")
+    s["q"] *= q
+    s["k"] *= k
+    s["v"] = (s["v"].clamp(-3, 3) * v).to(BF16)
+    check(call(s), definition(s), BF16)
+
+
 @pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
 @pytest.mark.parametrize("T", [1, 33])
 @pytest.mark.parametrize("tau", [1e-39, 1e-30, 1e6])
