@@ -88,6 +88,16 @@ def _view(name, t, packed_ok=True):
     raise RelPosError(f"{name} must be [B, H, N, d]" + (" or packed [T, H, d]" if packed_ok else ""))
 
 
+def _overlap(a, b):
+    """Whether two tensors share memory for sure: the same first element, or dense ones that
+    meet.  (Views that lie side by side in one buffer do not, and are not looked into.)"""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    p, q = a.data_ptr(), b.data_ptr()
+    return p == q or (a.is_contiguous() and b.is_contiguous() and p < q + b.numel() * b.element_size()
+                      and q < p + a.numel() * a.element_size())
+
+
 # ---------------------------------------------------------------- rotary embedding
 @dataclass(frozen=True)
 class RotaryMap:
@@ -165,8 +175,8 @@ def relpos_rotary(q, k=None, positions=None, *, rotary: RotaryMap, inverse: bool
     q, k: fp16, bf16 or fp32 CUDA tensors [B, H, N, d] of any strides with a
     contiguous last dimension, or packed [T, H, d]; they share all but the
     head count.  positions: int32 or int64 [N] or [B, N] (packed: [T]), None for
-    0 .. N - 1.  out: (q_out, k_out), which may be q and k themselves.  Returns the
-    turned q, or (q, k)."""
+    0 .. N - 1.  out: (q_out, k_out), which may be q and k themselves, each its own
+    input, but overlap nothing else.  Returns the turned q, or (q, k)."""
     dt, dev = q.dtype, q.device
     if dt not in _DTYPES or not q.is_cuda:
         raise RelPosError(f"q must be a float16, bfloat16 or float32 CUDA tensor, not {dt} on {dev}")
@@ -185,6 +195,12 @@ def relpos_rotary(q, k=None, positions=None, *, rotary: RotaryMap, inverse: bool
         pos_bs = positions.stride(0) if positions.dim() == 2 else 0
     if out is not None and (not isinstance(out, (tuple, list)) or len(out) != (1 if k is None else 2)):
         raise RelPosError("out must hold one tensor for each input")
+    if out is not None:
+        # q and k are turned in one launch, in no order
+        if any(y.data_ptr() != x.data_ptr() and _overlap(y, x) for x, y in zip((q, k), out)):
+            raise RelPosError("an output is its own input or does not overlap it")
+        if k is not None and (_overlap(out[0], out[1]) or _overlap(out[0], k) or _overlap(out[1], q)):
+            raise RelPosError("the outputs must not overlap one another, nor the other input")
     yq, blocks, x_q = _rotary_tensor(q, H, st, None if out is None else out[0])
     if k is not None:
         _cuda("k", k, dt, dev)
@@ -373,6 +389,8 @@ def kv_cache_read(cache: KVCache, page_table, cu_seqlens, *, total_tokens: Optio
             _cuda(name, t, dtype, dev)
             if not t.is_contiguous() or t.dim() != 3 or t.shape[0] < total_tokens or t.shape[1:] != (cache.kv_heads, cache.d):
                 raise RelPosError("out must be contiguous [total_tokens, kv_heads, d]")
+        if _overlap(k, v):
+            raise RelPosError("the outputs must not overlap")
     if dtype is None and not cache.coded:
         dtype = cache.dtype
     if dtype not in (torch.float16, torch.bfloat16):

@@ -269,7 +269,7 @@ int relpos_check_noalloc(relpos_stream_t stream, int32_t* device_status);
  * B = 1, N = T, stride_h = d, stride_n = H d. */
 typedef struct {
   const void* x;             /* device, read */
-  void* y;                   /* device, written: x itself (same strides), or no overlap with x */
+  void* y;                   /* device, written: x itself (same strides), or no overlap with any x or the other y */
   int32_t H, pad;
   int64_t x_stride_b, x_stride_h, x_stride_n;
   int64_t y_stride_b, y_stride_h, y_stride_n;
@@ -400,9 +400,9 @@ int relpos_tree_workspace_size(const relpos_tree_args* a, size_t* bytes);
  * where cached token j has position j, and node u has position
  * lengths[b] + (set bits of its mask) - 1, its depth in the tree.  T = 1 is
  * plain decoding.  A relation term of -inf hides its keys; finite ones count up to
- * 2^26 / (tau log2 e) in size; value scales of an 8-bit cache count from 2^-100 up.  With the same inputs the result does not depend on what
- * else runs, and equal calls give equal bits.  workspace: device, 256-byte
- * aligned, contents ignored; calls that may overlap on the GPU need workspaces
+ * 2^26 / (tau log2 e) in size; value scales of an 8-bit cache count from 2^-100 up.
+ * With the same inputs the result does not depend on what else runs, and equal calls
+ * give equal bits.  workspace: device, 256-byte aligned, contents ignored; calls that may overlap on the GPU need workspaces
  * of their own.  Its first word is a status word (relpos_check_workspace): the kernel
  * that takes more than 64 rows (H / kv_heads x T) over a 16-bit cache bounds its waits as
  * the layer's do.  Errors: INVALID_ARG (also for more than 2^30 tiles of 64 keys over all
