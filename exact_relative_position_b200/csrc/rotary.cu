@@ -147,6 +147,7 @@ cudaError_t go(const RotaryParams& p, cudaStream_t s) {
   // 8 (16 left too few threads: 151 us in place of 140)
   int hpt = (int)(threads * Ht / (148LL * 512));
   hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : hpt;
+  if (Ht > hpt * 65535) hpt = (Ht + 65534) / 65535;   // a grid's rows; two tensors have up to 131070 heads
   const int hy = (Ht + hpt - 1) / hpt;
   dim3 grid((unsigned)((threads + 255) / 256), (unsigned)hy);
   if (threads < (1LL << 31)) rotary_kernel<T, V, true><<<grid, 256, 0, s>>>(p, pair_jobs, jobs, hpt);

@@ -402,8 +402,8 @@ int relpos_tree_workspace_size(const relpos_tree_args* a, size_t* bytes);
  * plain decoding.  A relation term of -inf hides its keys; finite ones count up to
  * 2^26 / (tau log2 e) in size; value scales of an 8-bit cache count from 2^-100 up.
  * With the same inputs the result does not depend on what else runs, and equal calls
- * give equal bits.  workspace: device, 256-byte aligned, contents ignored; calls that may overlap on the GPU need workspaces
- * of their own.  Its first word is a status word (relpos_check_workspace): the kernel
+ * give equal bits.  workspace: device, 256-byte aligned, contents ignored; calls that
+ * may overlap on the GPU need workspaces of their own.  Its first word is a status word (relpos_check_workspace): the kernel
  * that takes more than 64 rows (H / kv_heads x T) over a 16-bit cache bounds its waits as
  * the layer's do.  Errors: INVALID_ARG (also for more than 2^30 tiles of 64 keys over all
  * sequences, key heads and row blocks, counted at the page table's width), UNSUPPORTED,
