@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
   __shared__ const float* row_z[ROWS];                  // relation terms of a row at offset e_lo
   __shared__ unsigned long long row_mask[ROWS];         // nodes it attends (0: padding, or no row)
   __shared__ int row_depth[ROWS], node_depth[64];
+  __shared__ __align__(8) float row_kc[ROWS];           // bf16, 8-bit caches: tau log2 e times the row's power of two
   int* pre = reinterpret_cast<int*>(smem);              // [B + 1], rounded up to 128 bytes
   const uint32_t pre_bytes = (uint32_t)((p.B + 1) * 4 + 127) & ~127u;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -499,7 +500,6 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
     // ---- queries: B fragments in the permuted k order, row r8 of each tile
     uint32_t qb[NR][KS][2];
     constexpr bool POWERS = !WIDE && DT<QT>::kCoarse;   // rows of queries have powers of two
-    float kc[NR][2];                                    // scores of 8-bit keys: acc * scale_j * kc (base 2), rows 2 q + e
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       const int r = rb * ROWS + (wm * NR + n) * 8 + r8;
@@ -518,7 +518,6 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         qb[n][2 * u + 1][1] = w.w;
         if (POWERS) top = amax2(amax2(amax2(amax2(top, w.x), w.y), w.z), w.w);
       }
-      kc[n][0] = kc[n][1] = p.c2;
       if (POWERS) {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -528,14 +527,19 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int i = 0; i < 2; ++i) qb[n][ks][i] = to_half2<QT>(qb[n][ks][i], down);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) kc[n][e] *= pow2i(__shfl_sync(0xffffffffu, power, 4 * (2 * q4 + e)));
+        if (q4 == 0) row_kc[(wm * NR + n) * 8 + r8] = p.c2 * pow2i(power);
       }
     }
 
     // ---- rows 2 q and 2 q + 1 of each tile: their saturated relation terms
     __syncthreads();
     auto row_of = [&](int n, int e) { return (wm * NR + n) * 8 + 2 * q4 + e; };   // in the block
+    // what turns the products of rows 2 q and 2 q + 1 with a key's codes into base-2 scores, but for the key's scale
+    auto unit_of = [&](int n) {
+      if (!POWERS) return make_float2(p.c2, p.c2);
+      const uint2 w = lds64(smem_u32(&row_kc[row_of(n, 0)]));
+      return make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    };
     float zlow[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n)
@@ -598,12 +602,14 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       }
     };
 
-    // Unsaturated relation terms of a step's scores: looked up a step ahead where
-    // the registers for it are there (up to 16 rows to a warp)
+    // Unsaturated relation terms of a step's scores: looked up a step ahead where the
+    // registers for it are there (up to 16 rows to a warp; over 8-bit caches at d = 128 up to 8:
+    // 16 trees of 61 over up to 8192 keys, 32 / 8 heads, int8, 534 us against 554 with them, and
+    // with one relation row per offset, 4 trees over 4096 keys, 79 against 82)
     struct Terms {
       float v[NR][SG][4];
     };
-    constexpr bool AHEAD = NR <= 2;
+    constexpr bool AHEAD = NR <= 2 && (WIDE || NR == 1 || D < 128);
     auto terms_of = [&](int kf, Terms& z) {             // kf: the step's first key
 #pragma unroll
       for (int n = 0; n < NR; ++n)
@@ -671,49 +677,31 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       }
       float rsv[SG][2];                                 // 1 / value scale of the thread's keys
       if (!WIDE) {
-        bool unit_scale = false;
+        float2 kc[NR];
 #pragma unroll
-        for (int g = 0; g < SG; ++g)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            rsv[g][j] = __uint_as_float(lds32(sk + 2 * HALF + (KW + ko + 16 * g + key0 + 2 * j) * 4));
-            unit_scale = unit_scale || rsv[g][j] == 1.f;
-          }
-        if (__any_sync(0xffffffffu, unit_scale)) {      // rows of zeros?  A quad looks at its keys' codes
-#pragma unroll
-          for (int g = 0; g < SG; ++g)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t any = 0;
-#pragma unroll
-              for (int u = 0; u < CPR / 4; ++u) {
-                const uint4 w = lds128(sv + chunk_at<CPR, WIDE, true>(ko + 16 * g + key0 + 2 * j, 4 * u + q4));
-                any |= w.x | w.y | w.z | w.w;
-              }
-              if (FMT == RELPOS_CACHE_E4M3) any &= 0x7f7f7f7fu;   // -0 is a zero
-              any |= __shfl_xor_sync(0xffffffffu, any, 1);
-              any |= __shfl_xor_sync(0xffffffffu, any, 2);
-              if (any == 0 && rsv[g][j] == 1.f) rsv[g][j] = kZeroRowScale;
-            }
-        }
+        for (int n = 0; n < NR; ++n) kc[n] = unit_of(n);
 #pragma unroll
         for (int g = 0; g < SG; ++g)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t a = sk + 2 * HALF + (ko + 16 * g + key0 + 2 * j) * 4;
             const float ks = __uint_as_float(lds32(a));
-            float v = rsv[g][j];
+            float v = __uint_as_float(lds32(a + KW * 4));
             v = v < 0x1p-100f ? 0x1p-100f : v;          // not fmaxf, which would drop the NaN of a spoilt row
             const float lg = lg2(v);
             rsv[g][j] = rcp(v);
+            // two rows at a time, so that the rows' own factors cost few instructions
+            const float2 ks2 = make_float2(ks, ks), lg2v = make_float2(lg, lg);
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& x = s[n][g][2 * j + e];
-                if (EASY) x = fmaf(x, ks * kc[n][e], lg + zlow[n][e]);
-                else x = fmaf(x, ks * kc[n][e], p.z ? lg + z.v[n][g][2 * j + e] : lg);
-              }
+            for (int n = 0; n < NR; ++n) {
+              const float2 f = __fmul2_rn(ks2, kc[n]);
+              float2 a = lg2v;
+              if (EASY) a = __fadd2_rn(a, make_float2(zlow[n][0], zlow[n][1]));
+              else if (p.z) a = __fadd2_rn(a, make_float2(z.v[n][g][2 * j], z.v[n][g][2 * j + 1]));
+              const float2 x = __ffma2_rn(make_float2(s[n][g][2 * j], s[n][g][2 * j + 1]), f, a);
+              s[n][g][2 * j] = x.x;
+              s[n][g][2 * j + 1] = x.y;
+            }
           }
       }
       if (!EASY && !full) {
@@ -837,6 +825,29 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       const uint32_t sk = stage0 + (uint32_t)stage * GSTAGE, sv = sk + HALF;
       const int k0 = tile * TK + wn * KW;
       const bool full = (full_stages >> stage) & 1u;
+      if (!WIDE) {
+        // value rows of zeros (scale 1, all codes 0) get their scale in the stage, once a tile (looking
+        // in every step cost 1 to 2%); warps that share the keys write the same
+#pragma unroll
+        for (int i = 0; i < LR; ++i) {
+          const int kl = 32 * i + lane;
+          const uint32_t at = sk + 2 * HALF + (KW + kl) * 4;
+          const bool unit = (KW % 32 == 0 || kl < KW) && __uint_as_float(lds32(at)) == 1.f;
+          if (__any_sync(0xffffffffu, unit)) {
+            if (unit) {
+              uint32_t any = 0;
+#pragma unroll 1
+              for (int ch = 0; ch < CPR; ++ch) {
+                const uint4 w = lds128(sv + chunk_at<CPR, WIDE, true>(kl, ch));
+                any |= w.x | w.y | w.z | w.w;
+              }
+              if (FMT == RELPOS_CACHE_E4M3) any &= 0x7f7f7f7fu;   // -0 is a zero
+              if (any == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(kZeroRowScale) : "memory");
+            }
+            __syncwarp();
+          }
+        }
+      }
 #pragma unroll 1
       for (int ko = 0; ko < KW; ko += TL::SK) {
         if (full && !unsaturated(k0 + ko)) {
@@ -934,7 +945,8 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
           const int u = u0 + key0 + 2 * j;
           const int du = u < p.T ? node_depth[u] : 0;
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
+          for (int n = 0; n < NR; ++n) {
+            const float2 kc = unit_of(n);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = row_of(n, e);
@@ -943,9 +955,10 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
               if (p.z) x += row_z[r][iclamp(du - row_depth[r], p.e_lo, p.e_hi) - p.e_lo];
               const bool keep = u < p.T && ((mk >> (u & 63)) & 1ull);
               float& y = s[n][2 * j + e];
-              y = keep ? fmaf(y, ks[j] * kc[n][e], x) : -INFINITY;
+              y = keep ? fmaf(y, ks[j] * (e ? kc.y : kc.x), x) : -INFINITY;
               lm[n][e] = fmaxf(lm[n][e], y);
             }
+          }
         }
         new_max(lm);
         uint32_t pb[NR][2];
