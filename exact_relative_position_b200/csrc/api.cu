@@ -900,7 +900,6 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
     p->aq = a->aq; p->bias = a->b;
     p->aq_hs = a->table_per_head ? (long long)p->R * a->cache.d : 0;
     p->z_scale = wide_cache(a->cache.format) ? 1.f : p->c2;
-    p->z_limit = 0x1p26f / p->c2;
     p->z_h = a->aq ? zw * a->T : zw;
     p->z_t = a->aq ? zw : 0;
     p->z_b = a->aq ? zw * a->T * a->H : 0;
@@ -908,6 +907,7 @@ int make_tree(const relpos_tree_args* a, TreeParams* p, TreeLayout* L) {
   }
   const int rows = p->G * a->T;
   p->rows_per_block = tree_rows_per_block(*p);
+  p->z_limit = p->rows_per_block == 256 ? (p->bf16 ? 0x1.8p30f : 0x1.8p27f) / p->c2 : 3.3e38f / std::max(p->c2, 1.f);
   p->row_blocks = (rows + p->rows_per_block - 1) / p->rows_per_block;
   // tiles (of 64 keys at least) are counted in 31 bits, and the next piece's start with them
   if ((cap / 64 + 4) * a->B * a->cache.kv_heads * p->row_blocks > 0x3fffffffLL) return RELPOS_ERR_INVALID_ARG;

@@ -6,10 +6,11 @@ namespace relpos {
 namespace tree {
 namespace {
 
-// A finite term is bounded to 2^26 in base-2 units (e^-4.6e7, where a weight is 0 next to any
-// other): a table may hide keys with the lowest number of its type, and the exponents of a
-// tile that is hidden altogether are s c2 - m with m = s c2 rounded, which is off by half a
-// unit of m's last place: 4 at 2^26, infinite weights further out.  An infinite term stays.
+// A finite term is bounded so that tau log2 e times it is finite, too: a table may hide keys
+// with the lowest number of its type, and no maximum can be subtracted from -inf.  The
+// many-row kernel's exponents are s c2 - m with m = s c2 rounded, off by half a unit of m's
+// last place: its terms end at 1.5 x 2^27 in base 2, where fp16 weights are still within 2^8
+// of their own (bf16: 1.5 x 2^30, 2^64).  An infinite term stays.
 __device__ __forceinline__ float term(const TreeParams& p, float x) {
   if (fabsf(x) <= 3.4028235e38f) x = fminf(fmaxf(x, -p.z_limit), p.z_limit);
   return x * p.z_scale;
@@ -128,6 +129,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   const int nt = pre[b + 1] - pre[b];
   const int in_b = at - pre[b] * line.items, item = in_b / nt, tile = in_b - item * nt;
   const int start = at - tile, before = line.quantum * blockIdx.x;
+  // base-2 units of the maxima: the narrow kernel's scores over a 16-bit cache are without tau log2 e
+  const float unit = wide && ROWS != 256 ? p.c2 : 1.f;
   const bool mine = at < line.total && tile > 0 && start >= before;
   const int c0 = blockIdx.x, c1 = (start + nt - 1) / line.quantum;
   const int hkv = item / p.row_blocks, rb = item - hkv * p.row_blocks;
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
           lk = slot(k0 + c)[ROWS * D + ROWS + r];
         }
       }
-      const float f = ex2(mk - safe(m));
+      const float f = ex2((mk - safe(m)) * unit);
       float lf = lk * f;
 #pragma unroll
       for (int q = 1; q < GL; q <<= 1) lf += __shfl_xor_sync(0xffffffffu, lf, q);
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
         add(fi, *reinterpret_cast<const float4*>(slot(k0 + i) + (long long)r * D + 4 * c));
       }
     }
-    if (r0 + tid / GL < n) store_row(p, b, hkv, rb * ROWS + r, c, o, m, l);
+    if (r0 + tid / GL < n) store_row(p, b, hkv, rb * ROWS + r, c, o, m * unit, l);
   }
 }
 

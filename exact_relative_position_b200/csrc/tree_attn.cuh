@@ -89,7 +89,7 @@ __device__ __forceinline__ float rcp(float x) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Sum-order-preserving join of (m, l): exponent base 2, -inf for nothing yet.
+// Sum-order-preserving join of (m, l): -inf for nothing yet.
 __device__ __forceinline__ float safe(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ---------------------------------------------------------------- the line of tiles
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
     auto new_max = [&](const float (&lm)[NR][2]) {
       bool up = false;
 #pragma unroll
-      for (int n = 0; n < NR; ++n) up = up || lm[n][0] > mrow[n][0] + slack || lm[n][1] > mrow[n][1] + slack;
+      for (int n = 0; n < NR; ++n) up = up || lm[n][0] - mrow[n][0] > slack || lm[n][1] - mrow[n][1] > slack;
       if (!__any_sync(0xffffffffu, up)) return;
 #pragma unroll
       for (int n = 0; n < NR; ++n)
@@ -736,13 +736,16 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
       uint32_t pb[NR][SG][2];
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        const float m0 = safe(mrow[n][0]) * unit, m1 = safe(mrow[n][1]) * unit;
+        // the difference first: s c2 - m c2 would be off by half a unit of m c2's last place, which
+        // beyond 2^27 (keys hidden by large negative biases) no 16-bit weight survives
+        const float2 m2 = make_float2(-safe(mrow[n][0]), -safe(mrow[n][1])), unit2 = make_float2(unit, unit);
 #pragma unroll
         for (int g = 0; g < SG; ++g)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float w0 = ex2(WIDE ? fmaf(s[n][g][2 * j], p.c2, -m0) : s[n][g][2 * j] - m0);
-            const float w1 = ex2(WIDE ? fmaf(s[n][g][2 * j + 1], p.c2, -m1) : s[n][g][2 * j + 1] - m1);
+            float2 x = __fadd2_rn(make_float2(s[n][g][2 * j], s[n][g][2 * j + 1]), m2);
+            if (WIDE) x = __fmul2_rn(x, unit2);
+            const float w0 = ex2(x.x), w1 = ex2(x.y);
             lrow[n][0] = WIDE ? lrow[n][0] + w0 : fmaf(w0, rsv[g][j], lrow[n][0]);
             lrow[n][1] = WIDE ? lrow[n][1] + w1 : fmaf(w1, rsv[g][j], lrow[n][1]);
             pb[n][g][j] = transpose8(DT<MT16>::pack(w0, w1));
@@ -1011,7 +1014,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         const int r = (wm * NR + n) * 8 + 2 * q4 + e;
         if (r8 == 0) {
-          sm_m[wn][r] = mrow[n][e] * unit;
+          sm_m[wn][r] = mrow[n][e];
           sm_l[wn][r] = l;
         }
       }
@@ -1034,7 +1037,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WN; ++w) m = fmaxf(m, sm_m[w][r]);
-        const float f = ex2(mrow[n][e] * unit - safe(m));
+        const float f = ex2((mrow[n][e] - safe(m)) * unit);
 #pragma unroll
         for (int i = 0; i < MTD; ++i)
 #pragma unroll
@@ -1052,7 +1055,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 #pragma unroll
         for (int w = 0; w < WN; ++w) m = fmaxf(m, sm_m[w][r]);
 #pragma unroll
-        for (int w = 0; w < WN; ++w) l += sm_l[w][r] * ex2(sm_m[w][r] - safe(m));
+        for (int w = 0; w < WN; ++w) l += sm_l[w][r] * ex2((sm_m[w][r] - safe(m)) * unit);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WN; ++w) {
@@ -1067,7 +1070,7 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
             slot[ROWS * D + ROWS + r] = l;
           }
         } else {
-          store_row(p, b, hkv, gr, c, o, m, l);
+          store_row(p, b, hkv, gr, c, o, m * unit, l);
         }
       }
       __syncthreads();                                  // the stage (at the end: rows and sums, too) is free again

@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const __grid_con
         for (int u = 0; u < 8; ++u) pm[u] = fmaxf(pm[u], x[120 + u]);
         const float mx = max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
         const float m_new = fmaxf(m_run, mx * c2 + rowc);
-        const bool grow = m_new > m_run + kSlack;
+        const bool grow = m_new - m_run > kSlack;      // (false for two infinities)
         if (__any_sync(0xffffffffu, grow)) {
           const float alpha = grow ? ex2(m_run - m_new) : 1.f;
           if (t > s.t0) {                               // the tile before has left O: its P V came before these scores

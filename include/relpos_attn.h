@@ -399,8 +399,9 @@ int relpos_tree_workspace_size(const relpos_tree_args* a, size_t* bytes);
  *   S_ij = tau (q_i.k_j + q_i.aQ[phi(p_j - p_i)] + b[phi(p_j - p_i)])
  * where cached token j has position j, and node u has position
  * lengths[b] + (set bits of its mask) - 1, its depth in the tree.  T = 1 is
- * plain decoding.  A relation term of -inf hides its keys; finite ones count up to
- * 2^26 / (tau log2 e) in size; value scales of an 8-bit cache count from 2^-100 up.
+ * plain decoding.  A relation term of -inf hides its keys; with more than 64 rows
+ * (H / kv_heads x T) over a 16-bit cache, finite ones count up to 1.5 x 2^27 / (tau log2 e) in
+ * size (bf16: 1.5 x 2^30).  Value scales of an 8-bit cache count from 2^-100 up.
  * With the same inputs the result does not depend on what else runs, and equal calls
  * give equal bits.  workspace: device, 256-byte aligned, contents ignored; calls that
  * may overlap on the GPU need workspaces of their own.  Its first word is a status word (relpos_check_workspace): the kernel

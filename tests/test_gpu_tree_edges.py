@@ -218,3 +218,25 @@ def test_a_tau_whose_base_2_form_is_infinite_is_refused():
         s["tau"] = bad
         with pytest.raises(rp.RelPosError):
             call(s)
+
+
+@pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS, ids=ROW_IDS)
+@pytest.mark.parametrize("low", [-1e6, -1e9])
+@pytest.mark.parametrize("tau", [None, 1.0])
+def test_a_large_bias_on_every_key_leaves_weights_and_lse(dt, fmt, H, Hkv, T, d, low, tau):
+    # the same bias on all keys: the weights are those without it up to the rounding of the scores, the LSE is lower by it
+    s = make(B=2, H=H, Hkv=Hkv, T=T, d=d, lens=[700, 15], dt=dt, fmt=fmt, map=rp.RelPosMap("truncated", clip=20), b=True, tree="tree")
+    s["b"][:] = low
+    if tau is not None:
+        s["tau"] = tau
+    o, lse = call(s)
+    # scores carry rounding of 2^-24 of |bias| (64 at 1e9), so O is only an average of the values; the LSE is the bias, the
+    # logarithm of at most 764 equal weights and the scores' own size away from it
+    vmax = float(max(s["v"].abs().max(), (s["cache"].v.float().abs() * (1 if s["cache"].v_scale is None else s["cache"].v_scale[..., None])).max()))
+    assert bool(torch.isfinite(o).all()) and float(o.abs().max()) <= vmax * (1 + 2.0 ** -7)
+    # (the many-row kernel's terms end at 1.5 x 2^27 in base 2, 1.5 x 2^30 in bf16)
+    end = math.log(2) * (1.5 * 2.0 ** (30 if dt == BF16 else 27) if fmt == dt and H // Hkv * T > 64 else math.inf)
+    low = max(low, -end / s["tau"])
+    own = s["tau"] * (8 * d ** 0.5 * 12 + 2.0 ** -22 * abs(low)) + 7
+    assert float((lse.double() - s["tau"] * low).abs().max()) <= own + 2.0 ** -22 * abs(low) * s["tau"]
