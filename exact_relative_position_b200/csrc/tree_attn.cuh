@@ -482,14 +482,12 @@ __global__ void __launch_bounds__(128, TL::BPS) tree_kernel(const __grid_constan
 
     // ---- the rows of the item
     if (tid < ROWS) {
-      const int r = rb * ROWS + tid;
-      unsigned long long mk = 0;
-      const float* z = p.z;
-      if (r < R) {
-        const int t = r / p.G, h = hkv * p.G + (r - t * p.G);
-        mk = node_mask(p, b, t);
-        z += b * p.z_b + h * p.z_h + t * p.z_t;
-      }
+      // a row that no query has attends nothing, and reads the last query's relation terms: it
+      // votes on moving the maxima, which terms that nobody wrote must not decide
+      const int r = min(rb * ROWS + tid, R - 1);
+      const int t = r / p.G, h = hkv * p.G + (r - t * p.G);
+      const unsigned long long mk = rb * ROWS + tid < R ? node_mask(p, b, t) : 0ull;
+      const float* z = p.z + (b * p.z_b + h * p.z_h + t * p.z_t);
       row_mask[tid] = mk;
       row_depth[tid] = max(__popcll(mk) - 1, 0);
       row_z[tid] = z;

@@ -240,3 +240,20 @@ def test_a_large_bias_on_every_key_leaves_weights_and_lse(dt, fmt, H, Hkv, T, d,
     low = max(low, -end / s["tau"])
     own = s["tau"] * (8 * d ** 0.5 * 12 + 2.0 ** -22 * abs(low)) + 7
     assert float((lse.double() - s["tau"] * low).abs().max()) <= own + 2.0 ** -22 * abs(low) * s["tau"]
+
+
+@pytest.mark.parametrize("dt,fmt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("H,Hkv,T,d", [(1, 1, 33, 64), (2, 1, 11, 128), (4, 4, 3, 64), (8, 1, 31, 64), (8, 1, 8, 128)], ids=["r33", "r22", "r3", "r248", "r64"])
+def test_nothing_depends_on_what_the_workspace_held(dt, fmt, H, Hkv, T, d):
+    # rows of a tile that no query has must not vote on the maxima by relation terms that nobody wrote: sequence 0 is
+    # empty, so most of its terms are left out
+    s = make(B=3, H=H, Hkv=Hkv, T=T, d=d, lens=[0, 303, 1], dt=dt, fmt=fmt, map=rp.RelPosMap("identity"), aq="head", b=True)
+    need = rp.tree_workspace_size(s["cache"], 3, T, H, s["table"].shape[1], aq=True, b=True, map=s["map"])
+    want = None
+    for fill in (0.0, 1e30, -1e30, 50.0, math.inf, -math.inf, math.nan):
+        ws = torch.full((need // 4,), fill, device="cuda")
+        got = call(s, workspace=ws)
+        if want is None:
+            want = got
+            check(want, definition(s), dt)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), fill
