@@ -20,8 +20,10 @@
 // up to eight query heads to a key head fills the tile.  With so few rows each
 // loaded element feeds few multiply-adds and the kernel is bound by memory;
 // 128-row tcgen05 tiles would run mostly empty.  64 single tokens over up to 8192
-// keys, 32 / 8 heads of 128: e4m3 129 us (5.5 TB/s, 84% of a plain copy's rate); half
-// of them over bf16 116 us (91% of it).  More rows over a 16-bit cache: tree_wide.cu.
+// keys, 32 / 8 heads of 128: e4m3 126 us (5.6 TB/s, 86% of a plain copy's rate); 32 of
+// them over bf16 113 us (6.0 TB/s, 94% of it).  More rows over a 16-bit cache: tree_wide.cu.
+// 61-node trees over 8 bits stay here, in blocks of 64 rows that each read and expand the
+// cache: 16 of them over up to 8192 keys, 32 / 8 heads of 128, e4m3 with bf16 queries 531 us.
 //
 // Order of the operands.  An MMA sums over k in any order and names its rows in
 // any order, as long as both operands agree.  Each lane of a quad therefore
@@ -44,8 +46,9 @@
 // A value row of zeros is stored with scale 1.  Taken at that, a key that is attended
 // strongly and holds zeros (they are common where a model parks its attention) would set
 // m_i far above what the other keys, with scales of 2^-10, add to O, and their 16-bit weights
-// would be subnormal or 0.  Such a row enters at 2^-64: it adds nothing to O at any scale,
-// and its share of l_i, kept in fp32, is exact for the others' scales up to 2^30.
+// would be subnormal or 0.  Such a row enters at 2^-64, so that it sets the maximum only where
+// it leaves the others less than 2^-50 of their values, and its share of l_i, kept in fp32, is
+// exact for the others' scales up to 2^30.
 // bf16 queries enter in fp16 after an exact power-of-two scaling of each row to a
 // largest element in [2^14, 2^15): a power of the row's own, since what a padding node or
 // another head holds must not cost this one its precision.
@@ -1125,7 +1128,9 @@ cudaError_t run_tiling(const TreeParams& p, cudaStream_t s) {
 // halves the votes and loop code of a step: int8, d = 64, 16 rows 41.7 to 35.1 us (at three
 // blocks to an SM in place of four, for the registers), 32 rows 72 to 66; int8, d = 128, 8
 // rows 115 to 106; 16-bit caches at d = 128 have no registers for it.  Two warps to 16 rows
-// each beat one with 32 (72 to 66 us: the wider warp spills).
+// each beat one with 32 (72 to 66 us: the wider warp spills).  What still spills: 16 rows at d =
+// 128 over 8 bits (132 bytes of stores, 220 to 248 with bf16 queries, whose look-ups of
+// factors come on top), 64 rows there 80 to 84.
 template <int D, bool WIDE> struct Tilings;
 template <bool WIDE> struct Tilings<64, WIDE> {
   using R8 = Tiling<64, 1, 4, 1, 32, 32, WIDE ? 2 : 3, WIDE ? 3 : 4>;

@@ -5,9 +5,10 @@
 // is 256 query rows (two tiles of 128) of one key head, so that each K/V tile
 // feeds four 128-row MMAs and the work per byte is that of a dense attention
 // layer: the tensor and exponential units bound it, not memory.  16 trees of 61 nodes
-// over up to 8192 keys, 32 / 8 heads of 128: 171 us, 490 TFLOP/s; a tile of keys takes 2.6 us
+// over up to 8192 keys, 32 / 8 heads of 128: 169 us, 495 TFLOP/s; a tile of keys takes 2.6 us
 // where the tensor unit's share is 1.2: the softmax warpgroups and the MMAs wait for
-// one another's hand-overs.
+// one another's hand-overs.  A softmax thread holds a row's 128 scores: 108 bytes spill at d =
+// 128, 128 at d = 64.
 //
 // Warp roles of a block (one to an SM, walking its piece of the line):
 //   warp 0        MMA issuer (one thread); allocates the tensor memory

@@ -111,7 +111,9 @@ class RotaryMap:
       "ntk":    base * factor ** (rotary_dim / (rotary_dim - 2)) as the base;
       "yarn":   w_i kept where a trained context of original_length turns it more than
                 beta_fast times, divided by factor where fewer than beta_slow times, mixed
-                linearly between (YaRN, Peng et al. 2023), and magnitude 0.1 ln(factor) + 1.
+                linearly in the number of turns between (YaRN, Peng et al. 2023), and magnitude
+                0.1 ln(factor) + 1.  A model that was run with a mix linear in the pair's index
+                instead brings its own `frequencies`.
     magnitude, where given, multiplies the turned columns in place of the
     scaling's own; frequencies, where given, replace the w_i.
     """
@@ -446,7 +448,8 @@ def relpos_tree_attention(q, k, v, cache: KVCache, page_table, lengths, aq=None,
     node the position lengths[b] + its depth (set bits - 1).
 
     aq ([R, d] or [H, R, d], q's dtype) and b ([H, R] float32) with `map` add the
-    relation terms of relpos_attention at those positions; tables of max_seqlen as
+    relation terms of relpos_attention at those positions (a term of -inf hides its
+    keys); tables of max_seqlen as
     there (by default a bucketed or truncated map needs no more than the pages
     hold, and an identity map's is (R + 1) / 2).  Inference only: no autograd.
     Calls that may overlap on the GPU need workspaces of their own; by default each
