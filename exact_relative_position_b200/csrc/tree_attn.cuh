@@ -33,6 +33,11 @@
 // which makes the four rows of V that a lane pairs up consecutive keys.  P^T
 // goes from the score layout to the operand layout by movmatrix.
 //
+// Weights enter P V in 16 bits, as in the layer's forward: the cache's own type, fp16 over 8
+// bits; their sums stay fp32.  Split weights would double the MMAs of P V to take the error of
+// O against 64 bits from 0.00023 to 0.00021 (fp16) and from 0.0021 to 0.0017 (bf16), where the
+// rounding of O itself is the rest.
+//
 // The row maximum is moved only when a score exceeds it by 2^8: weights stay
 // within 2^8, far from fp16's range, and most steps skip the rescaling of O and
 // the reduction over lanes.
